@@ -18,8 +18,9 @@ LIB_SAN = os.path.join(HERE, "liblq_san.so")
 LIB_BOUNDS = os.path.join(HERE, "liblq_bounds.so")
 SAN_FLAGS = ["-Xcompiler", "-fsanitize=address,-fsanitize=undefined,-fno-omit-frame-pointer,-g",
              "-lasan", "-lubsan"]
-SOURCES = ["lq_api.cu", "lq_quant.cu", "lq_gemm.cu", "lq_gemv.cu", "lq_cta.cu", "lq_noalloc.cu"]
-HEADERS = ["lq_common.cuh"]
+SOURCES = ["lq_api.cu", "lq_quant.cu", "lq_gemm.cu", "lq_gemv.cu", "lq_cta.cu", "lq_noalloc.cu",
+           "lq_dense.cu", "lq_distill.cu", "lq_dense_api.cu"]
+HEADERS = ["lq_common.cuh", "lq_dense.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

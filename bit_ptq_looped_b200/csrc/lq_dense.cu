@@ -1,0 +1,1167 @@
+// Dense (unquantized) products around the looped linear, on the 5th-generation
+// tensor cores (sm_100a), operands bf16 or f16:
+//
+//   dense        y  = act(x W^T + b) + r          (optionally z = x W^T + b)
+//   gated        h  = act(x Wg^T + bg) * (x Wu^T + bu)   (optionally both factors)
+//   dx           dx = dz W        (gated: [dg | du] [Wg ; Wu])
+//   dw           dw = dz^T x      (gated: both weights in one product)
+//
+// All four are one product C = A B^T over a contraction index kept in 64-wide
+// blocks; they differ in which operand is contiguous along the contraction
+// (K-major: x, W, dz rows) and which across it (MN-major: W in dx, both
+// operands of dw), and in the epilogue.  tcgen05.mma reads either form
+// straight from the 128-byte-swizzled tile that TMA wrote, so no operand is
+// ever transposed in memory.
+//
+// k_dense_gemm is persistent (one CTA per SM): a TMA warp fills a ring of
+// stages, an MMA warp issues kind::f16 MMAs (float32 accumulators in TMEM, two
+// accumulators so that a tile's epilogue overlaps the next tile's products),
+// and the epilogue warps read TMEM, apply bias, activation, product and
+// residual in float32, round once, and write whole 64-byte or longer row
+// pieces through a swizzled shared-memory tile.
+//
+// Up to 16 rows (decode) the product is a stream of the weights:
+// k_dense_rows reads each weight once with 16-byte loads and multiplies with
+// mma.sync (16 weight rows x 8 tokens), the contraction split over the warps
+// of a block.
+//
+// Every mbarrier wait is bounded; on expiry the kernel records
+// LQ_ERR_DEVICE_TIMEOUT, stops all roles, frees its TMEM and returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "lq_dense.cuh"
+
+namespace lq {
+namespace {
+
+constexpr int BM = 128;  // accumulator rows of a CTA (TMEM lanes)
+constexpr int BK = 64;   // contraction elements per stage: one 128-byte row of 16-bit values
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
+
+__device__ int g_dense_status = 0;
+
+// Bounded wait that ignores the abort flag (teardown: no copy or MMA of this
+// CTA is in flight when it exits).
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      atomicExch(&g_dense_status, (int)LQ_ERR_DEVICE_TIMEOUT);
+      return;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// element types
+// ---------------------------------------------------------------------------
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__nv_bfloat16> {
+  static constexpr uint32_t kFormat = 1;  // instruction descriptor: bf16
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ float load(const uint16_t* p) {
+    return __uint_as_float((uint32_t)*p << 16);
+  }
+  static __device__ __forceinline__ uint16_t round(float v) {
+    return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  }
+};
+template <>
+struct Elem<__half> {
+  static constexpr uint32_t kFormat = 0;  // f16
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 unpack(uint32_t w) {
+    return __half22float2(*reinterpret_cast<__half2*>(&w));
+  }
+  static __device__ __forceinline__ float load(const uint16_t* p) {
+    return __half2float(__ushort_as_half(*p));
+  }
+  static __device__ __forceinline__ uint16_t round(float v) {
+    return __half_as_ushort(__float2half_rn(v));
+  }
+};
+
+// ---------------------------------------------------------------------------
+// activations, float32
+// ---------------------------------------------------------------------------
+// logistic function through the hardware exponential and reciprocal (a few
+// units in the last place of float32, far below the 16-bit output rounding);
+// exp overflow gives 1/inf = 0
+__device__ __forceinline__ float logistic(float z) {
+  return __fdividef(1.f, 1.f + __expf(-z));
+}
+constexpr float kGeluC = 0.7978845608028654f;  // sqrt(2 / pi)
+// 0.5 (1 + tanh(v)) = logistic(2 v): no cancellation for large negative v
+__device__ __forceinline__ float gelu_tanh_gate(float z) {
+  return logistic(2.f * kGeluC * (z + 0.044715f * z * z * z));
+}
+// the normal distribution function, 0.5 (1 + erf(z / sqrt 2)), without the
+// cancellation of that sum at large negative z
+__device__ __forceinline__ float phi_cdf(float z) { return 0.5f * erfcf(-0.7071067811865476f * z); }
+
+template <int kAct>
+__device__ __forceinline__ float act_fn(float z) {
+  if (kAct == LQ_ACT_RELU) return z > 0.f ? z : (z != z ? z : 0.f);
+  if (kAct == LQ_ACT_SILU) return z * logistic(z);
+  if (kAct == LQ_ACT_GELU) return z * phi_cdf(z);
+  if (kAct == LQ_ACT_GELU_TANH) return z * gelu_tanh_gate(z);
+  return z;
+}
+
+// act(z) and act'(z)
+template <int kAct>
+__device__ __forceinline__ void act_grad(float z, float& a, float& da) {
+  if (kAct == LQ_ACT_RELU) {
+    a = z > 0.f ? z : (z != z ? z : 0.f);
+    da = z > 0.f ? 1.f : (z != z ? z : 0.f);
+  } else if (kAct == LQ_ACT_SILU) {
+    const float s = logistic(z);
+    a = z * s;
+    da = s + a * (1.f - s);
+  } else if (kAct == LQ_ACT_GELU) {
+    const float p = phi_cdf(z);
+    a = z * p;
+    da = p + z * __expf(-0.5f * z * z) * 0.3989422804014327f;  // 1 / sqrt(2 pi)
+  } else if (kAct == LQ_ACT_GELU_TANH) {
+    const float s = gelu_tanh_gate(z);
+    a = z * s;
+    // past |z| = 100 the factor a (1 - s) is zero; the bound keeps z^2 finite
+    da = s + 2.f * a * (1.f - s) * kGeluC * (1.f + 3.f * 0.044715f * fminf(z * z, 1e4f));
+  } else {
+    a = z;
+    da = 1.f;
+  }
+}
+
+// v[i] = act(v[i]) for n values, the activation chosen once per call
+template <int kN>
+__device__ __forceinline__ void apply_act(int act, float (&v)[kN]) {
+  switch (act) {
+    case LQ_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = act_fn<LQ_ACT_RELU>(v[i]);
+      break;
+    case LQ_ACT_SILU:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = act_fn<LQ_ACT_SILU>(v[i]);
+      break;
+    case LQ_ACT_GELU:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = act_fn<LQ_ACT_GELU>(v[i]);
+      break;
+    case LQ_ACT_GELU_TANH:
+#pragma unroll
+      for (int i = 0; i < kN; ++i) v[i] = act_fn<LQ_ACT_GELU_TANH>(v[i]);
+      break;
+    default:
+      break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// tcgen05 wrappers
+// ---------------------------------------------------------------------------
+// Shared-memory descriptors of 128-byte-swizzled 16-bit tiles.
+// K-major: rows of 64 contraction elements (128 B), 8-row atoms 1024 B apart
+// (stride offset); the leading offset is not used.
+// MN-major: the tile is a row of chunks of 64 row indices (128 B) by 64
+// contraction steps; 8-step atoms are 1024 B apart (stride offset), chunks
+// 8192 B apart (leading offset).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, bool mn_major) {
+  uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((mn_major ? 8192u : 16u) >> 4) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1u << 46;  // descriptor version (sm_100)
+  d |= (uint64_t)2u << 61;  // 128-byte swizzle
+  return d;
+}
+
+// kind::f16: F32 accumulator, operand format, operand majors, N >> 3, M >> 4
+__host__ __device__ constexpr uint32_t instr_desc(uint32_t fmt, bool a_mn, bool b_mn, int m,
+                                                  int n) {
+  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+__device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// ---------------------------------------------------------------------------
+// the tile kernel
+// ---------------------------------------------------------------------------
+enum Epi : int {
+  kEpiDense = 0,  // act(acc + bias) + residual, optionally the pre-activation
+  kEpiGated = 1,  // act(acc_g + bias_g) * (acc_u + bias_u), optionally both factors
+  kEpiStore = 2,  // round and store
+  kEpiF32 = 3,    // float32, optionally added to what is there
+};
+
+struct GemmParams {
+  int64_t M, N;    // extents of the output (N per factor when gated)
+  int64_t ldo;     // elements between output rows
+  int n_kb, n_kb1; // contraction blocks; those of the first operand pair
+  int act;
+  int accumulate;
+  int vec;         // rows are 16-byte aligned: 16-byte stores
+  const uint16_t* bias;
+  const uint16_t* bias2;
+  const uint16_t* res;
+  void* out;
+  // output rows from `split` on go to out2 (row r to out2 + (r - split) * ldo),
+  // rows in [rows1, split) are padding and are not written
+  void* out2;
+  int64_t split, rows1;
+  uint16_t* aux;   // z, or the gate factor g
+  uint16_t* aux2;  // the up factor u
+};
+
+template <int kBN, int kEpi>
+struct Cfg {
+  static constexpr int kEpiWarps = kBN >= 128 ? 8 : 4;
+  // columns an epilogue warp handles: its column half of the tile (of each
+  // factor's half when gated)
+  static constexpr int kCols = kBN / (kEpiWarps / 4) / (kEpi == kEpiGated ? 2 : 1);
+  // columns per shared-memory unit: 128-byte rows, or 64-byte ones
+  static constexpr int kUnit = (kEpi == kEpiF32 || kCols < 64) ? 32 : 64;
+  static constexpr uint32_t kStageA = BM * BK * 2, kStageB = kBN * BK * 2;
+  static constexpr uint32_t kStageBytes = kStageA + kStageB;
+  static constexpr uint32_t kStaging = kEpiWarps * 32 * 128;
+  static constexpr int kStages = (int)((226u * 1024u - 1024u - 512u - kStaging) / kStageBytes);
+  static constexpr uint32_t kOffB = kStages * kStageA;
+  static constexpr uint32_t kOffStaging = kOffB + kStages * kStageB;
+  static constexpr uint32_t kOffBar = kOffStaging + kStaging;
+  static constexpr uint32_t kOffMisc = kOffBar + (2 * kStages + 5) * 8;
+  static constexpr uint32_t kSmem = kOffMisc + 16 + 1024;
+  static constexpr int kThreads = 32 * (kEpiWarps + 2);
+  static constexpr int kTmemCols = 2 * kBN;
+};
+
+// 32 x kUnit values of one warp in shared memory: row = lane, 16-byte pieces
+// XOR-swizzled so that both the row-per-lane accesses and the row-piece-per-
+// lane accesses are free of bank conflicts
+template <int kRowBytes>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+  return kRowBytes == 128 ? row * 128 + ((piece ^ (row & 7)) << 4)
+                          : row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
+}
+
+struct RowMap {
+  int64_t M, rows1, split;
+  char* out;
+  char* out2;
+  int64_t row_bytes;
+  __device__ __forceinline__ char* operator()(int64_t r) const {
+    if (r >= M) return nullptr;
+    if (r < rows1) return out + r * row_bytes;
+    if (r < split) return nullptr;
+    return out2 + (r - split) * row_bytes;
+  }
+};
+
+// shared-memory unit -> global rows.  kEsz: bytes per element
+template <int kRowBytes, int kEsz>
+__device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, const RowMap& map,
+                                           int64_t row0, int64_t col0, int64_t N, bool vec) {
+  constexpr int kPieces = kRowBytes / 16;
+  constexpr int kPer = 16 / kEsz;  // elements per piece
+  if (vec) {  // whole pieces: N is a multiple of a piece
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
+      char* dst = map(row0 + row);
+      const int64_t c = col0 + pc * kPer;
+      if (dst && c < N)
+        *reinterpret_cast<uint4*>(dst + c * kEsz) =
+            *reinterpret_cast<const uint4*>(stg + piece_at<kRowBytes>(row, pc));
+    }
+    return;
+  }
+  constexpr int kElems = kRowBytes / kEsz;
+  for (int row = 0; row < 32; ++row) {
+    char* dst = map(row0 + row);
+    if (!dst) continue;
+#pragma unroll
+    for (int e = 0; e < kElems; e += 32) {
+      const int i = e + lane;
+      const int64_t c = col0 + i;
+      if (c >= N) continue;
+      const unsigned char* src =
+          stg + piece_at<kRowBytes>(row, i / kPer) + (i % kPer) * kEsz;
+      if (kEsz == 2)
+        *reinterpret_cast<uint16_t*>(dst + c * 2) = *reinterpret_cast<const uint16_t*>(src);
+      else
+        *reinterpret_cast<uint32_t*>(dst + c * 4) = *reinterpret_cast<const uint32_t*>(src);
+    }
+  }
+}
+
+// global rows -> shared-memory unit (16-bit elements); what lies outside the
+// matrix is left as it is
+template <int kRowBytes>
+__device__ __forceinline__ void fill_unit(unsigned char* stg, int lane, const uint16_t* src,
+                                          int64_t ld, int64_t row0, int64_t col0, int64_t M,
+                                          int64_t N, bool vec) {
+  constexpr int kPieces = kRowBytes / 16;
+  if (vec) {
+    uint4 v[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
+      const int64_t r = row0 + row, c = col0 + pc * 8;
+      v[j] = make_uint4(0, 0, 0, 0);
+      if (r < M && c < N) v[j] = *reinterpret_cast<const uint4*>(src + r * ld + c);
+    }
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
+      *reinterpret_cast<uint4*>(stg + piece_at<kRowBytes>(row, pc)) = v[j];
+    }
+    return;
+  }
+  for (int row = 0; row < 32; ++row) {
+    const int64_t r = row0 + row;
+    if (r >= M) continue;
+#pragma unroll
+    for (int e = 0; e < kRowBytes / 2; e += 32) {
+      const int i = e + lane;
+      const int64_t c = col0 + i;
+      if (c < N)
+        *reinterpret_cast<uint16_t*>(stg + piece_at<kRowBytes>(row, i / 8) + (i % 8) * 2) =
+            src[r * ld + c];
+    }
+  }
+}
+
+// v[i] += bias[col + i] (columns past N: unchanged)
+template <typename T>
+__device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t* bias, int64_t col,
+                                         int64_t N) {
+  if (col + 32 <= N) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 8) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(bias + col + i));
+      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = Elem<T>::unpack(q[e]);
+        v[i + 2 * e] += f.x;
+        v[i + 2 * e + 1] += f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (col + i < N) v[i] += Elem<T>::load(bias + col + i);
+  }
+}
+
+template <typename T, int kRowBytes>
+__device__ __forceinline__ void put_row(unsigned char* stg, int lane, int c0, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint4 w;
+    w.x = Elem<T>::pack(v[8 * i], v[8 * i + 1]);
+    w.y = Elem<T>::pack(v[8 * i + 2], v[8 * i + 3]);
+    w.z = Elem<T>::pack(v[8 * i + 4], v[8 * i + 5]);
+    w.w = Elem<T>::pack(v[8 * i + 6], v[8 * i + 7]);
+    *reinterpret_cast<uint4*>(stg + piece_at<kRowBytes>(lane, c0 / 8 + i)) = w;
+  }
+}
+
+template <typename T, int kRowBytes>
+__device__ __forceinline__ void add_row(const unsigned char* stg, int lane, int c0,
+                                        float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = *reinterpret_cast<const uint4*>(stg + piece_at<kRowBytes>(lane, c0 / 8 + i));
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = Elem<T>::unpack(q[e]);
+      v[8 * i + 2 * e] += f.x;
+      v[8 * i + 2 * e + 1] += f.y;
+    }
+  }
+}
+
+__device__ __forceinline__ void load_acc(uint32_t taddr, float (&v)[32]) {
+  uint32_t r[32];
+  tmem_ld_32x32b_x32(taddr, r);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// tile t -> (tile row, tile column): bands of 16 tile rows, column by column
+// inside a band, so that the tiles in flight share operand rows and columns
+__device__ __forceinline__ void tile_at(int t, int tm, int tn, int& im, int& in) {
+  const int band = t / (16 * tn), first = band * 16;
+  const int h = min(16, tm - first), r = t - band * 16 * tn;
+  im = first + r % h;
+  in = r / h;
+}
+
+template <typename T, int kBN, bool kAMn, bool kBMn, int kEpi>
+__global__ void __launch_bounds__(Cfg<kBN, kEpi>::kThreads, 1)
+    k_dense_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
+                 const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
+                 const __grid_constant__ GemmParams P) {
+  using C = Cfg<kBN, kEpi>;
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  unsigned char* gbase = smem_raw + (base - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar_full = base + C::kOffBar;
+  const uint32_t bar_empty = bar_full + C::kStages * 8;
+  const uint32_t bar_accf = bar_empty + C::kStages * 8;
+  const uint32_t bar_acce = bar_accf + 2 * 8;
+  const uint32_t bar_drain = bar_acce + 2 * 8;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
+  constexpr int kTileN = kEpi == kEpiGated ? kBN / 2 : kBN;  // output columns of a tile
+  const int tm = (int)((P.M + BM - 1) / BM), tn = (int)((P.N + kTileN - 1) / kTileN);
+  const int n_tiles = tm * tn;
+
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(bar_full + 8 * s, 1);
+      mbar_init(bar_empty + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(bar_accf + 8 * b, 1);
+      mbar_init(bar_acce + 8 * b, C::kEpiWarps);
+    }
+    mbar_init(bar_drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // everything below reads or writes global memory
+
+  if (warp == C::kEpiWarps) {
+    // ---- TMA producer
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+        int im, in;
+        tile_at(t, tm, tn, im, in);
+        const int m0 = im * BM, n0 = in * kTileN;
+        for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
+          const int st = it % C::kStages;
+          if (!mbar_wait_bounded(bar_empty + 8 * st, ((uint32_t)(it / C::kStages) & 1u) ^ 1u,
+                                 abort_flag, &g_dense_status, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          const bool first = kb < P.n_kb1;
+          const CUtensorMap* a = first ? &tmA : &tmA2;
+          const CUtensorMap* b = first ? &tmB : &tmB2;
+          const int k0 = (first ? kb : kb - P.n_kb1) * BK;
+          const uint32_t full = bar_full + 8 * st;
+          const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
+          mbar_arrive_expect_tx(full, C::kStageBytes);
+          if (kAMn) {
+#pragma unroll
+            for (int c = 0; c < BM / 64; ++c) tma_load_2d(sa + c * 8192, a, full, m0 + 64 * c, k0);
+          } else {
+            tma_load_2d(sa, a, full, k0, m0);
+          }
+          if (kBMn) {
+#pragma unroll
+            for (int c = 0; c < kBN / 64; ++c) tma_load_2d(sb + c * 8192, b, full, n0 + 64 * c, k0);
+          } else if (kEpi == kEpiGated) {
+            tma_load_2d(sb, &tmB, full, k0, n0);
+            tma_load_2d(sb + C::kStageB / 2, &tmB2, full, k0, n0);
+          } else {
+            tma_load_2d(sb, b, full, k0, n0);
+          }
+        }
+      }
+      for (int i = max(0, it - C::kStages); i < it; ++i)
+        wait_drain(bar_full + 8 * (i % C::kStages), (uint32_t)(i / C::kStages) & 1u);
+    }
+  } else if (warp == C::kEpiWarps + 1) {
+    // ---- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc = instr_desc(Elem<T>::kFormat, kAMn, kBMn, BM, kBN);
+      // bytes between consecutive 16-wide contraction steps of a stage
+      constexpr uint32_t stepA = kAMn ? 2048u : 32u, stepB = kBMn ? 2048u : 32u;
+      int it = 0, j = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++j) {
+        const int buf = j & 1;
+        if (!mbar_wait_bounded(bar_acce + 8 * buf, ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag,
+                               &g_dense_status, kWaitLimitNs))
+          break;
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
+        for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
+          const int st = it % C::kStages;
+          if (!mbar_wait_bounded(bar_full + 8 * st, (uint32_t)(it / C::kStages) & 1u, abort_flag,
+                                 &g_dense_status, kWaitLimitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
+#pragma unroll
+          for (int i = 0; i < BK / 16; ++i)
+            umma_f16(d, smem_desc(sa + stepA * i, kAMn), smem_desc(sb + stepB * i, kBMn), idesc,
+                     (kb | i) ? 1u : 0u);
+          umma_commit(bar_empty + 8 * st);
+        }
+        if (ok) umma_commit(bar_accf + 8 * buf);
+      }
+      umma_commit(bar_drain);
+      wait_drain(bar_drain, 0u);
+    }
+  } else {
+    // ---- epilogue: warp w reads TMEM lanes 32 (w % 4).. and column part w / 4
+    const int q = warp & 3, part = warp >> 2;
+    unsigned char* stg = gbase + C::kOffStaging + warp * 4096;
+    constexpr int kRowBytes = C::kUnit * (kEpi == kEpiF32 ? 4 : 2);
+    int j = 0;
+    for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++j) {
+      int im, in;
+      tile_at(t, tm, tn, im, in);
+      const int buf = j & 1;
+      const int64_t row0 = (int64_t)im * BM + 32 * q;
+      const int64_t n0 = (int64_t)in * kTileN;
+      const bool live = row0 < P.M;
+      if (!mbar_wait_bounded(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag,
+                             &g_dense_status, kWaitLimitNs))
+        break;
+      tc_fence_after();
+      const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kBN);
+      const RowMap map = {P.M,          P.rows1,       P.split,
+                          (char*)P.out, (char*)P.out2, P.ldo * (kEpi == kEpiF32 ? 4 : 2)};
+      for (int u = 0; u < C::kCols; u += C::kUnit) {
+        const int tc = part * C::kCols + u;  // tile column of this unit
+        const int64_t col = n0 + tc;
+        if (!live || col >= P.N) continue;
+        if (kEpi == kEpiDense && P.aux) {
+          for (int c = 0; c < C::kUnit; c += 32) {
+            float v[32];
+            load_acc(acc + tc + c, v);
+            if (P.bias) add_bias<T>(v, P.bias, col + c, P.N);
+            put_row<T, kRowBytes>(stg, lane, c, v);
+          }
+          __syncwarp();
+          const RowMap za = {P.M, P.M, P.M, (char*)P.aux, nullptr, P.ldo * 2};
+          flush_unit<kRowBytes, 2>(stg, lane, za, row0, col, P.N, P.vec);
+          __syncwarp();
+        }
+        if (kEpi == kEpiGated && P.aux) {
+          for (int f = 0; f < 2; ++f) {
+            for (int c = 0; c < C::kUnit; c += 32) {
+              float v[32];
+              load_acc(acc + f * kTileN + tc + c, v);
+              const uint16_t* b = f ? P.bias2 : P.bias;
+              if (b) add_bias<T>(v, b, col + c, P.N);
+              put_row<T, kRowBytes>(stg, lane, c, v);
+            }
+            __syncwarp();
+            const RowMap za = {P.M, P.M, P.M, (char*)(f ? P.aux2 : P.aux), nullptr, P.ldo * 2};
+            flush_unit<kRowBytes, 2>(stg, lane, za, row0, col, P.N, P.vec);
+            __syncwarp();
+          }
+        }
+        if (kEpi == kEpiDense && P.res) {
+          fill_unit<kRowBytes>(stg, lane, P.res, P.ldo, row0, col, P.M, P.N, P.vec);
+          __syncwarp();
+        }
+        for (int c = 0; c < C::kUnit; c += 32) {
+          float v[32];
+          load_acc(acc + tc + c, v);
+          if (kEpi == kEpiDense) {
+            if (P.bias) add_bias<T>(v, P.bias, col + c, P.N);
+            apply_act(P.act, v);
+            if (P.res) add_row<T, kRowBytes>(stg, lane, c, v);
+          }
+          if (kEpi == kEpiGated) {
+            if (P.bias) add_bias<T>(v, P.bias, col + c, P.N);
+            apply_act(P.act, v);
+            float w[32];
+            load_acc(acc + kTileN + tc + c, w);
+            if (P.bias2) add_bias<T>(w, P.bias2, col + c, P.N);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= w[i];
+          }
+          if (kEpi == kEpiF32) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(stg + piece_at<128>(lane, i)) =
+                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+          } else {
+            put_row<T, kRowBytes>(stg, lane, c, v);
+          }
+        }
+        __syncwarp();
+        if (kEpi == kEpiF32) {
+          if (P.accumulate) {
+            // each lane adds its own pieces of what is there
+            for (int row = 0; row < 32; ++row) {
+              const char* src = map(row0 + row);
+              if (src && col + lane < P.N) {
+                float* p = reinterpret_cast<float*>(stg + piece_at<128>(row, lane / 4)) + lane % 4;
+                *p += reinterpret_cast<const float*>(src)[col + lane];
+              }
+            }
+            __syncwarp();
+          }
+          flush_unit<kRowBytes, 4>(stg, lane, map, row0, col, P.N, P.vec);
+        } else {
+          flush_unit<kRowBytes, 2>(stg, lane, map, row0, col, P.N, P.vec);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, C::kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// up to 16 rows: stream the weights
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1, bool bf16) {
+  if (bf16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct RowsParams {
+  const uint16_t* x;
+  const uint16_t* w;
+  const uint16_t* w2;
+  const uint16_t* bias;
+  const uint16_t* bias2;
+  const uint16_t* res;
+  uint16_t* y;
+  uint16_t* aux;
+  uint16_t* aux2;
+  int M, N, K, act;
+};
+
+constexpr int kRowsWarps = 8;
+constexpr int kRowsUnroll = 4;
+
+// A block owns 16 weight rows (of each factor when gated); its warps take
+// 32-wide contraction blocks in turn.  The contraction order inside a 32-wide
+// block is permuted so that every operand load is one 16-byte vector: lane
+// (g, t) holds elements 8t..8t+7 of weight rows g and g + 8 and of token g,
+// and calls the first four "k = 2t, 2t+1, 2t+8, 2t+9" of a first MMA, the
+// others of a second; both operands use the same permutation, so the sum is
+// unchanged.  The warps' partial sums are added in shared memory in warp order.
+template <typename T, int kNT, bool kGated>
+__global__ void __launch_bounds__(32 * kRowsWarps) k_dense_rows(const RowsParams P) {
+  constexpr int kF = kGated ? 2 : 1;
+  constexpr bool kBf16 = Elem<T>::kFormat == 1;
+  __shared__ float part[kRowsWarps][kF][16][8 * kNT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * 16;
+  pdl_trigger();
+  pdl_wait();
+  float acc[kF][kNT][4];
+#pragma unroll
+  for (int f = 0; f < kF; ++f)
+#pragma unroll
+    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[f][j][i] = 0.f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int n_blk = (P.K + 31) / 32;
+  for (int b0 = warp; b0 < n_blk; b0 += kRowsWarps * kRowsUnroll) {
+    uint4 a[kRowsUnroll][kF][2], xb[kRowsUnroll][kNT];
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u) {
+      const int k = (b0 + u * kRowsWarps) * 32 + 8 * t;
+      const bool in = k < P.K;  // K is a multiple of 8
+#pragma unroll
+      for (int f = 0; f < kF; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int n = n0 + g + 8 * h;
+          a[u][f][h] = zero;
+          if (in && n < P.N)
+            a[u][f][h] =
+                __ldg(reinterpret_cast<const uint4*>((f ? P.w2 : P.w) + (int64_t)n * P.K + k));
+        }
+#pragma unroll
+      for (int j = 0; j < kNT; ++j) {
+        const int m = 8 * j + g;
+        xb[u][j] = zero;
+        if (in && m < P.M)
+          xb[u][j] = __ldg(reinterpret_cast<const uint4*>(P.x + (int64_t)m * P.K + k));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u)
+#pragma unroll
+      for (int f = 0; f < kF; ++f)
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) {
+          const uint4 p = a[u][f][0], r = a[u][f][1], c = xb[u][j];
+          mma_16x8x16(acc[f][j], p.x, r.x, p.y, r.y, c.x, c.y, kBf16);
+          mma_16x8x16(acc[f][j], p.z, r.z, p.w, r.w, c.z, c.w, kBf16);
+        }
+  }
+#pragma unroll
+  for (int f = 0; f < kF; ++f)
+#pragma unroll
+    for (int j = 0; j < kNT; ++j) {
+      float(*p)[8 * kNT + 1] = part[warp][f];
+      p[g][8 * j + 2 * t] = acc[f][j][0];
+      p[g][8 * j + 2 * t + 1] = acc[f][j][1];
+      p[g + 8][8 * j + 2 * t] = acc[f][j][2];
+      p[g + 8][8 * j + 2 * t + 1] = acc[f][j][3];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 16 * 8 * kNT; i += 32 * kRowsWarps) {
+    const int r = i % 16, m = i / 16, n = n0 + r;
+    if (n >= P.N || m >= P.M) continue;
+    float v[1] = {0.f}, s2 = 0.f;
+#pragma unroll
+    for (int w = 0; w < kRowsWarps; ++w) {
+      v[0] += part[w][0][r][m];
+      if (kGated) s2 += part[w][kF - 1][r][m];
+    }
+    const int64_t o = (int64_t)m * P.N + n;
+    if (P.bias) v[0] += Elem<T>::load(P.bias + n);
+    if (P.aux) P.aux[o] = Elem<T>::round(v[0]);
+    apply_act(P.act, v);
+    if (kGated) {
+      if (P.bias2) s2 += Elem<T>::load(P.bias2 + n);
+      if (P.aux2) P.aux2[o] = Elem<T>::round(s2);
+      v[0] *= s2;
+    } else if (P.res) {
+      v[0] += Elem<T>::load(P.res + o);
+    }
+    P.y[o] = Elem<T>::round(v[0]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dz from the output gradient, and the column sums of dz
+// ---------------------------------------------------------------------------
+struct GradParams {
+  const uint16_t* dy;
+  const uint16_t* z;   // gate (or only) pre-activation; null: no activation
+  const uint16_t* u;   // up factor (gated)
+  uint16_t* dz;        // M x ldz, null: not wanted (sums only)
+  float* sums;         // row blocks x (factors * N) partial column sums, or null
+  int64_t M, N, ldz;   // gated: du starts at column ldz / 2
+  int64_t rows;        // rows per row block
+  int act;
+};
+
+// A block covers 32 kVec columns of one row block: a thread owns kVec
+// neighbouring columns and every 8th row, keeps their float32 sums in
+// registers, and the eight row groups are added in shared memory in order.
+template <typename T, int kVec, bool kGated, int kAct>
+__global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
+  constexpr int kF = kGated ? 2 : 1;
+  __shared__ float red[8][kF][32 * kVec];
+  const int lane = threadIdx.x & 31, rg = threadIdx.x >> 5;
+  const int64_t half = kGated ? P.ldz / 2 : P.ldz;
+  const int64_t c0 = ((int64_t)blockIdx.x * 32 + lane) * kVec;
+  const int64_t r0 = (int64_t)blockIdx.y * P.rows, r1 = min(P.M, r0 + P.rows);
+  pdl_trigger();
+  pdl_wait();
+  float sum[kF][kVec];
+#pragma unroll
+  for (int f = 0; f < kF; ++f)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) sum[f][i] = 0.f;
+  if (c0 < half) {
+    for (int64_t r = r0 + rg; r < r1; r += 8) {
+      float dy[kVec], z[kVec], u[kVec], o[kF][kVec];
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) dy[i] = z[i] = u[i] = 0.f;
+      if (c0 < P.N) {  // kVec > 1: N is a multiple of kVec
+        const int64_t at = r * P.N + c0;
+        if (kVec == 8) {
+          const uint4 a = __ldg(reinterpret_cast<const uint4*>(P.dy + at));
+          uint4 b = make_uint4(0, 0, 0, 0), c = b;
+          if (kAct != LQ_ACT_NONE || kGated) b = __ldg(reinterpret_cast<const uint4*>(P.z + at));
+          if (kGated) c = __ldg(reinterpret_cast<const uint4*>(P.u + at));
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w},
+                         cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+          for (int e = 0; e < kVec / 2; ++e) {
+            const float2 fa = Elem<T>::unpack(aw[e & 3]), fb = Elem<T>::unpack(bw[e & 3]),
+                         fc = Elem<T>::unpack(cw[e & 3]);
+            dy[2 * e] = fa.x, dy[2 * e + 1] = fa.y;
+            z[2 * e] = fb.x, z[2 * e + 1] = fb.y;
+            u[2 * e] = fc.x, u[2 * e + 1] = fc.y;
+          }
+        } else {
+          dy[0] = Elem<T>::load(P.dy + at);
+          if (kAct != LQ_ACT_NONE || kGated) z[0] = Elem<T>::load(P.z + at);
+          if (kGated) u[0] = Elem<T>::load(P.u + at);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        float a, da;
+        act_grad<kAct>(z[i], a, da);
+        o[0][i] = kGated ? dy[i] * u[i] * da : dy[i] * da;
+        if (kGated) o[kF - 1][i] = dy[i] * a;
+        // columns past N are padding of the contraction: exactly zero
+        if (c0 + i >= P.N) o[0][i] = o[kF - 1][i] = 0.f;
+      }
+#pragma unroll
+      for (int f = 0; f < kF; ++f) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) sum[f][i] += o[f][i];
+        if (P.dz) {
+          uint16_t* dst = P.dz + r * P.ldz + f * half + c0;
+          if (kVec == 8) {
+            uint4 w;
+            w.x = Elem<T>::pack(o[f][0], o[f][1 % kVec]);
+            w.y = Elem<T>::pack(o[f][2 % kVec], o[f][3 % kVec]);
+            w.z = Elem<T>::pack(o[f][4 % kVec], o[f][5 % kVec]);
+            w.w = Elem<T>::pack(o[f][6 % kVec], o[f][7 % kVec]);
+            *reinterpret_cast<uint4*>(dst) = w;
+          } else {
+            *dst = Elem<T>::round(o[f][0]);
+          }
+        }
+      }
+    }
+  }
+  if (!P.sums) return;
+#pragma unroll
+  for (int f = 0; f < kF; ++f)
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) red[rg][f][lane * kVec + i] = sum[f][i];
+  __syncthreads();
+  for (int i = threadIdx.x; i < kF * 32 * kVec; i += 256) {
+    const int f = i / (32 * kVec), c = i % (32 * kVec);
+    const int64_t col = (int64_t)blockIdx.x * 32 * kVec + c;
+    if (col >= P.N) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += red[k][f][c];
+    P.sums[((int64_t)blockIdx.y * kF + f) * P.N + col] = s;
+  }
+}
+
+// the row blocks' partial sums, added in order
+template <typename T>
+__global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ sums, int64_t N, int nf,
+                                                  int blocks, void* out, void* out2, int f32,
+                                                  int accumulate) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  pdl_trigger();
+  pdl_wait();
+  if (c >= N * nf) return;
+  float s = 0.f;
+  for (int b = 0; b < blocks; ++b) s += sums[(int64_t)b * nf * N + c];
+  void* o = c < N ? out : out2;
+  if (!o) return;
+  const int64_t i = c < N ? c : c - N;
+  if (f32)
+    ((float*)o)[i] = accumulate ? ((float*)o)[i] + s : s;
+  else
+    ((uint16_t*)o)[i] = Elem<T>::round(s);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (PFN_cuTensorMapEncodeTiled_v12000)p;
+  });
+  return fn;
+}
+
+// rows x cols 16-bit matrix (cols contiguous, row stride ld elements), boxes of
+// 64 columns by box_rows rows, 128-byte swizzle, zeros outside
+bool make_map(CUtensorMap* map, const void* p, bool bf16, int64_t rows, int64_t cols, int64_t ld,
+              int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// one operand of a product: rows x contraction when K-major, contraction x
+// rows when MN-major
+struct Operand {
+  const void* p;
+  int64_t rows, k, ld;
+};
+
+bool operand_map(CUtensorMap* m, const Operand& o, bool mn, bool bf16, int tile_rows) {
+  return mn ? make_map(m, o.p, bf16, o.k, o.rows, o.ld, BK)
+            : make_map(m, o.p, bf16, o.rows, o.k, o.ld, tile_rows);
+}
+
+template <typename T, int kBN, bool kAMn, bool kBMn, int kEpi>
+cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
+                     const GemmParams& P, cudaStream_t s) {
+  using C = Cfg<kBN, kEpi>;
+  constexpr bool bf16 = Elem<T>::kFormat == 1;
+  constexpr int rowsB = kEpi == kEpiGated ? kBN / 2 : kBN;
+  CUtensorMap mA, mA2, mB, mB2;
+  if (!operand_map(&mA, a, kAMn, bf16, BM) || !operand_map(&mA2, a2, kAMn, bf16, BM) ||
+      !operand_map(&mB, b, kBMn, bf16, rowsB) || !operand_map(&mB2, b2, kBMn, bf16, rowsB))
+    return cudaErrorInvalidValue;
+  auto* k = k_dense_gemm<T, kBN, kAMn, kBMn, kEpi>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  constexpr int kTileN = kEpi == kEpiGated ? kBN / 2 : kBN;
+  const int64_t tiles = ((P.M + BM - 1) / BM) * ((P.N + kTileN - 1) / kTileN);
+  if (tiles > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_kernel(k, dim3((unsigned)std::min<int64_t>(tiles, num_sms())), dim3(C::kThreads),
+                       C::kSmem, s, true, mA, mA2, mB, mB2, P);
+}
+
+// Tile width.  A wide tile reads fewer operand bytes per product, a narrow one
+// fills more SMs: take the widest whose tiles still cover the SMs, else the
+// narrowest.
+template <typename T, bool kAMn, bool kBMn, int kEpi>
+cudaError_t pick_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
+                      const GemmParams& P, cudaStream_t s) {
+  constexpr int f = kEpi == kEpiGated ? 2 : 1;
+  const int64_t tm = (P.M + BM - 1) / BM;
+  auto tiles = [&](int bn) { return tm * ((P.N * f + bn - 1) / bn); };
+  if (tiles(256) >= num_sms()) return run_gemm<T, 256, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  if (tiles(128) >= num_sms()) return run_gemm<T, 128, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  return run_gemm<T, 64, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+}
+
+GemmParams base_params(int64_t M, int64_t N, int64_t kdim) {
+  GemmParams P{};
+  P.M = M;
+  P.N = N;
+  P.ldo = N;
+  P.n_kb = P.n_kb1 = (int)((kdim + BK - 1) / BK);
+  P.rows1 = P.split = M;
+  P.vec = N % 8 == 0;
+  return P;
+}
+
+template <typename T>
+cudaError_t run_rows(const RowsParams& P, bool gated, cudaStream_t s) {
+  const dim3 grid((unsigned)((P.N + 15) / 16)), block(32 * kRowsWarps);
+  if (gated)
+    return P.M <= 8 ? launch_kernel(k_dense_rows<T, 1, true>, grid, block, 0, s, true, P)
+                    : launch_kernel(k_dense_rows<T, 2, true>, grid, block, 0, s, true, P);
+  return P.M <= 8 ? launch_kernel(k_dense_rows<T, 1, false>, grid, block, 0, s, true, P)
+                  : launch_kernel(k_dense_rows<T, 2, false>, grid, block, 0, s, true, P);
+}
+
+template <typename T>
+cudaError_t forward(const DenseForward& d, cudaStream_t s) {
+  const bool gated = d.w2 != nullptr;
+  if (d.M <= kDenseRowsMax) {
+    RowsParams R{(const uint16_t*)d.x,    (const uint16_t*)d.w,     (const uint16_t*)d.w2,
+                 (const uint16_t*)d.bias, (const uint16_t*)d.bias2, (const uint16_t*)d.res,
+                 (uint16_t*)d.y,          (uint16_t*)d.aux,         (uint16_t*)d.aux2,
+                 (int)d.M,                (int)d.N,                 (int)d.K,
+                 d.act};
+    return run_rows<T>(R, gated, s);
+  }
+  GemmParams P = base_params(d.M, d.N, d.K);
+  P.act = d.act;
+  P.bias = (const uint16_t*)d.bias;
+  P.bias2 = (const uint16_t*)d.bias2;
+  P.res = (const uint16_t*)d.res;
+  P.out = d.y;
+  P.aux = (uint16_t*)d.aux;
+  P.aux2 = (uint16_t*)d.aux2;
+  const Operand x{d.x, d.M, d.K, d.K}, w{d.w, d.N, d.K, d.K};
+  if (gated) {
+    const Operand w2{d.w2, d.N, d.K, d.K};
+    return pick_gemm<T, false, false, kEpiGated>(x, x, w, w2, P, s);
+  }
+  return pick_gemm<T, false, false, kEpiDense>(x, x, w, w, P, s);
+}
+
+template <typename T, int kVec, bool kGated>
+cudaError_t act_grad_launch(const GradParams& P, dim3 grid, cudaStream_t s) {
+  switch (P.act) {
+    case LQ_ACT_RELU:
+      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_RELU>, grid, dim3(256), 0, s, true, P);
+    case LQ_ACT_SILU:
+      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_SILU>, grid, dim3(256), 0, s, true, P);
+    case LQ_ACT_GELU:
+      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_GELU>, grid, dim3(256), 0, s, true, P);
+    case LQ_ACT_GELU_TANH:
+      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_GELU_TANH>, grid, dim3(256), 0, s,
+                           true, P);
+    default:
+      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_NONE>, grid, dim3(256), 0, s, true, P);
+  }
+}
+
+template <typename T>
+cudaError_t backward(const DenseBackward& d, cudaStream_t s) {
+  const bool gated = d.gated;
+  const DenseBwdPlan pl = dense_bwd_plan(d.M, d.N, gated, d.act != LQ_ACT_NONE);
+  const bool products = d.dx || d.dw || d.dw2;
+  const bool sums = d.db || d.db2;
+  uint16_t* dz = (uint16_t*)d.ws;
+  float* part = (float*)((char*)d.ws + pl.dz_bytes);
+  const int nf = gated ? 2 : 1;
+  cudaError_t e;
+  if (sums || (products && pl.copy)) {
+    GradParams G{};
+    G.dy = (const uint16_t*)d.dy;
+    G.z = (const uint16_t*)d.z;
+    G.u = (const uint16_t*)d.u;
+    G.dz = products && pl.copy ? dz : nullptr;
+    G.sums = sums ? part : nullptr;
+    G.M = d.M;
+    G.N = d.N;
+    G.ldz = pl.ldz;
+    G.rows = pl.rows;
+    G.act = d.act;
+    const bool vec = d.N % 8 == 0;
+    const int64_t width = gated ? pl.ldz / 2 : pl.ldz, per = vec ? 256 : 32;
+    const dim3 grid((unsigned)((width + per - 1) / per), (unsigned)pl.row_blocks);
+    if (gated)
+      e = vec ? act_grad_launch<T, 8, true>(G, grid, s) : act_grad_launch<T, 1, true>(G, grid, s);
+    else
+      e = vec ? act_grad_launch<T, 8, false>(G, grid, s) : act_grad_launch<T, 1, false>(G, grid, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (sums) {
+    e = launch_kernel(k_col_sums<T>, dim3((unsigned)((d.N * nf + 255) / 256)), dim3(256), 0, s,
+                      true, (const float*)part, d.N, nf, pl.row_blocks, d.db, d.db2, d.f32,
+                      d.accumulate);
+    if (e != cudaSuccess) return e;
+  }
+  const void* dzp = pl.copy ? (const void*)dz : d.dy;
+  const int64_t half = gated ? pl.ldz / 2 : pl.ldz;
+  if (d.dx) {
+    GemmParams P = base_params(d.M, d.K, half);
+    P.out = d.dx;
+    const Operand a{dzp, d.M, half, pl.ldz};
+    const Operand b{d.w, d.K, d.N, d.K};
+    Operand a2 = a, b2 = b;
+    if (gated) {
+      a2.p = dz + half;
+      b2.p = d.w2;
+      P.n_kb = 2 * P.n_kb1;
+    }
+    e = pick_gemm<T, false, true, kEpiStore>(a, a2, b, b2, P, s);
+    if (e != cudaSuccess) return e;
+  }
+  if (d.dw || d.dw2) {
+    // output rows: the columns of dz; the padding columns between and after
+    // the factors are not written.  A factor that is not wanted is left out.
+    const bool only2 = !d.dw;
+    const int64_t rows = gated && d.dw && d.dw2 ? half + d.N : d.N;
+    GemmParams P = base_params(rows, d.K, d.M);
+    P.out = only2 ? d.dw2 : d.dw;
+    P.out2 = d.dw2;
+    P.rows1 = d.N;
+    P.split = rows > d.N ? half : rows;
+    P.accumulate = d.accumulate;
+    const Operand a{only2 ? (const void*)(dz + half) : dzp, rows, d.M, pl.ldz};
+    const Operand b{d.x, d.K, d.M, d.K};
+    e = d.f32 ? pick_gemm<T, true, true, kEpiF32>(a, a, b, b, P, s)
+              : pick_gemm<T, true, true, kEpiStore>(a, a, b, b, P, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_dense_forward(const DenseForward& d, cudaStream_t s) {
+  return d.dtype == LQ_BF16 ? forward<__nv_bfloat16>(d, s) : forward<__half>(d, s);
+}
+
+DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, bool gated, bool act) {
+  DenseBwdPlan p{};
+  // dz is its own matrix where it differs from dy, or where dy's rows do not
+  // start on 16-byte boundaries (a TMA source needs that)
+  p.copy = gated || act || N % 8 != 0;
+  const int64_t width = (N + BK - 1) / BK * BK;
+  p.ldz = p.copy ? width * (gated ? 2 : 1) : N;
+  p.dz_bytes = p.copy ? (M * p.ldz * 2 + 255) / 256 * 256 : 0;
+  // at most 256 row blocks of at least 64 rows
+  p.rows = std::max<int64_t>(64, (M + 255) / 256);
+  p.row_blocks = (int)((M + p.rows - 1) / p.rows);
+  p.sum_bytes = ((int64_t)p.row_blocks * N * (gated ? 2 : 1) * 4 + 255) / 256 * 256;
+  return p;
+}
+
+cudaError_t launch_dense_backward(const DenseBackward& d, cudaStream_t s) {
+  return d.dtype == LQ_BF16 ? backward<__nv_bfloat16>(d, s) : backward<__half>(d, s);
+}
+
+int take_dense_status() {
+  int v = 0, zero = 0;
+  if (cudaMemcpyFromSymbol(&v, g_dense_status, sizeof(int)) != cudaSuccess) return 0;
+  if (v) cudaMemcpyToSymbol(g_dense_status, &zero, sizeof(int));
+  return v;
+}
+
+}  // namespace lq

@@ -23,7 +23,10 @@ LIB_PATH = os.environ.get("LQ_LIB_PATH") or os.path.join(HERE, "liblq.so")
 LQ_OK, LQ_ERR_ARG, LQ_ERR_SHAPE, LQ_ERR_UNSUPPORTED, LQ_ERR_ALIGN = 0, 1, 2, 3, 4
 LQ_ERR_CUDA, LQ_ERR_DEVICE_TIMEOUT, LQ_ERR_NOMEM, LQ_ERR_WORKSPACE = 5, 6, 7, 8
 LQ_ERR_DEVICE_BOUNDS = 9
-LQ_F32, LQ_BF16 = 0, 1
+LQ_F32, LQ_BF16, LQ_F16 = 0, 1, 2
+LQ_ACT_NONE, LQ_ACT_RELU, LQ_ACT_SILU, LQ_ACT_GELU, LQ_ACT_GELU_TANH = 0, 1, 2, 3, 4
+LQ_ACTS = {"none": LQ_ACT_NONE, "relu": LQ_ACT_RELU, "silu": LQ_ACT_SILU, "gelu": LQ_ACT_GELU,
+           "gelu_tanh": LQ_ACT_GELU_TANH}
 LQ_OPEN, LQ_CHAIN = 0, 1
 
 STATUS_NAMES = {0: "LQ_OK", 1: "LQ_ERR_ARG", 2: "LQ_ERR_SHAPE", 3: "LQ_ERR_UNSUPPORTED",
@@ -60,6 +63,20 @@ SIGNATURES = {
     "lq_cta_apply": (_i32, [_vp, _i64, _vp, _i32, _vp, _vp]),
     "lq_cta_stack_workspace_bytes": (_i64, [_pp, _i32, _i64]),
     "lq_loop_stack_cta": (_i32, [_vp, _i32, _i64, _pp, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
+    "lq_dense_linear_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "lq_dense_linear": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp,
+                               _i64, _vp]),
+    "lq_dense_linear_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32]),
+    "lq_dense_linear_bwd": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp,
+                                   _vp, _i32, _i32, _vp, _i64, _vp]),
+    "lq_gated_linear_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "lq_gated_linear": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp,
+                               _vp, _vp, _i64, _vp]),
+    "lq_gated_linear_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "lq_gated_linear_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32,
+                                   _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i64, _vp]),
+    "lq_distill_loss": (_i32, [_vp, _i32, _i64, _i64, _vp, _i32, _vp, _i32, _i64, _vp, _vp, _f32,
+                               _vp, _vp, _vp]),
     "lq_check_device": (_i32, [_vp]),
     "lq_selftest_bounded_wait": (_i32, [_i64, _vp]),
     "lq_selftest_grid_wait": (_i32, [_i64, _vp, _vp]),
@@ -436,6 +453,230 @@ def lq_loop_stack_cta(x: torch.Tensor, layers: Sequence[Layer], T: int, cta: Cta
                                  _dev(y, "y"), _dev(ws, "ws"), ws.numel(), _stream(stream))
     _check(st, "lq_loop_stack_cta")
     return y
+
+
+# ---------------------------------------------------------------------------
+# dense products and the distillation loss
+# ---------------------------------------------------------------------------
+_DTYPE_CODES = {torch.float32: LQ_F32, torch.bfloat16: LQ_BF16, torch.float16: LQ_F16}
+
+
+def _code(t: torch.Tensor, name: str) -> int:
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype} of {name}")
+    return code
+
+
+def _mat(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Optional[int]:
+    """Device pointer of a contiguous tensor of this shape and dtype on this device."""
+    if t is None:
+        return None
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on_device(t: torch.Tensor, name: str, dims: int) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return t.device
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(ws: Optional[torch.Tensor], n: int, device, stream):
+    """(pointer, bytes, tensor to keep) of a workspace of n bytes."""
+    if n < 0:
+        raise ValueError("invalid shape")
+    if ws is None:
+        if n == 0:
+            return None, 0, None
+        ws = _empty(n, torch.uint8, device, stream)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError("the workspace must be contiguous and on the operands' device")
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+def lq_dense_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
+                    act: int = LQ_ACT_NONE, residual: Optional[torch.Tensor] = None,
+                    y: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
+                    want_z: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+    """y = act(x w^T + bias) + residual; returns (y, z), z the pre-activation that
+    the backward pass reads (None unless wanted).  x M x K, w N x K, bf16 or f16;
+    y may be the residual itself."""
+    dev = _on_device(x, "x", 2)
+    M, K = x.shape
+    N = w.shape[0]
+    dt = x.dtype
+    if y is None:
+        y = _empty((M, N), dt, dev, stream)
+    if z is None and want_z:
+        z = _empty((M, N), dt, dev, stream)
+    p_ws, n_ws, keep = _scratch(ws, lib().lq_dense_linear_workspace_bytes(M, N, K), dev, stream)
+    st = lib().lq_dense_linear(
+        _mat(x, "x", (M, K), dt, dev), _mat(w, "w", (N, K), dt, dev),
+        _mat(bias, "bias", (N,), dt, dev), _mat(residual, "residual", (M, N), dt, dev),
+        _code(x, "x"), M, N, K, act, _mat(y, "y", (M, N), dt, dev),
+        _mat(z, "z", (M, N), dt, dev), p_ws, n_ws, _stream(stream))
+    _check(st, "lq_dense_linear")
+    return y, z
+
+
+def _grad_out(given, want, shape, dtype, dev, stream, accumulate, name):
+    if given is not None:
+        return given
+    if not want:
+        return None
+    if accumulate:
+        raise ValueError(f"accumulating needs the {name} to add to")
+    return _empty(shape, dtype, dev, stream)
+
+
+def lq_dense_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torch.Tensor],
+                        z: Optional[torch.Tensor] = None, *, act: int = LQ_ACT_NONE,
+                        want_dx: bool = True, want_dw: bool = True, want_db: bool = False,
+                        dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                        db: Optional[torch.Tensor] = None, g_dtype: Optional[torch.dtype] = None,
+                        accumulate: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of lq_dense_linear: returns (dx, dw, db), None where not wanted.
+    g_dtype: type of dw and db (dy's, or float32); accumulate: add to the given
+    float32 dw and db."""
+    dev = _on_device(dy, "dy", 2)
+    M, N = dy.shape
+    if x is None and w is None:
+        raise ValueError("need x or w")
+    K = x.shape[1] if x is not None else w.shape[1]
+    dt = dy.dtype
+    if g_dtype is None:
+        g_dtype = dw.dtype if dw is not None else db.dtype if db is not None else dt
+    dx = _grad_out(dx, want_dx, (M, K), dt, dev, stream, False, "dx")
+    dw = _grad_out(dw, want_dw, (N, K), g_dtype, dev, stream, accumulate, "dw")
+    db = _grad_out(db, want_db, (N,), g_dtype, dev, stream, accumulate, "db")
+    n = lib().lq_dense_linear_bwd_workspace_bytes(M, N, K, act)
+    p_ws, n_ws, keep = _scratch(ws, n, dev, stream)
+    st = lib().lq_dense_linear_bwd(
+        _mat(dy, "dy", (M, N), dt, dev), _mat(z, "z", (M, N), dt, dev),
+        _mat(x, "x", (M, K), dt, dev), _mat(w, "w", (N, K), dt, dev), _code(dy, "dy"), M, N, K,
+        act, _mat(dx, "dx", (M, K), dt, dev), _mat(dw, "dw", (N, K), g_dtype, dev),
+        _mat(db, "db", (N,), g_dtype, dev), _DTYPE_CODES.get(g_dtype, -1),
+        1 if accumulate else 0, p_ws, n_ws, _stream(stream))
+    _check(st, "lq_dense_linear_bwd")
+    return dx, dw, db
+
+
+def lq_gated_linear(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor,
+                    bg: Optional[torch.Tensor] = None, bu: Optional[torch.Tensor] = None, *,
+                    act: int = LQ_ACT_SILU, h: Optional[torch.Tensor] = None,
+                    g: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None,
+                    want_gu: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+    """h = act(x wg^T + bg) * (x wu^T + bu); returns (h, g, u), the two factors
+    before the activation where the backward pass will read them (else None)."""
+    dev = _on_device(x, "x", 2)
+    M, K = x.shape
+    N = wg.shape[0]
+    dt = x.dtype
+    if h is None:
+        h = _empty((M, N), dt, dev, stream)
+    if want_gu:
+        g = _empty((M, N), dt, dev, stream) if g is None else g
+        u = _empty((M, N), dt, dev, stream) if u is None else u
+    p_ws, n_ws, keep = _scratch(ws, lib().lq_gated_linear_workspace_bytes(M, N, K), dev, stream)
+    st = lib().lq_gated_linear(
+        _mat(x, "x", (M, K), dt, dev), _mat(wg, "wg", (N, K), dt, dev),
+        _mat(wu, "wu", (N, K), dt, dev), _mat(bg, "bg", (N,), dt, dev),
+        _mat(bu, "bu", (N,), dt, dev), _code(x, "x"), M, N, K, act,
+        _mat(h, "h", (M, N), dt, dev), _mat(g, "g", (M, N), dt, dev),
+        _mat(u, "u", (M, N), dt, dev), p_ws, n_ws, _stream(stream))
+    _check(st, "lq_gated_linear")
+    return h, g, u
+
+
+def lq_gated_linear_bwd(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
+                        x: Optional[torch.Tensor], wg: Optional[torch.Tensor],
+                        wu: Optional[torch.Tensor], *, act: int = LQ_ACT_SILU,
+                        want_dx: bool = True, want_dw: bool = True, want_db: bool = False,
+                        dx: Optional[torch.Tensor] = None, dwg: Optional[torch.Tensor] = None,
+                        dwu: Optional[torch.Tensor] = None, dbg: Optional[torch.Tensor] = None,
+                        dbu: Optional[torch.Tensor] = None,
+                        g_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                        ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients of lq_gated_linear: returns (dx, dwg, dwu, dbg, dbu), None where
+    not wanted.  g_dtype and accumulate as in lq_dense_linear_bwd."""
+    dev = _on_device(dh, "dh", 2)
+    M, N = dh.shape
+    if x is None and wg is None:
+        raise ValueError("need x or wg")
+    K = x.shape[1] if x is not None else wg.shape[1]
+    dt = dh.dtype
+    if g_dtype is None:
+        g_dtype = next((t.dtype for t in (dwg, dwu, dbg, dbu) if t is not None), dt)
+    dx = _grad_out(dx, want_dx, (M, K), dt, dev, stream, False, "dx")
+    dwg = _grad_out(dwg, want_dw, (N, K), g_dtype, dev, stream, accumulate, "dwg")
+    dwu = _grad_out(dwu, want_dw, (N, K), g_dtype, dev, stream, accumulate, "dwu")
+    dbg = _grad_out(dbg, want_db, (N,), g_dtype, dev, stream, accumulate, "dbg")
+    dbu = _grad_out(dbu, want_db, (N,), g_dtype, dev, stream, accumulate, "dbu")
+    n = lib().lq_gated_linear_bwd_workspace_bytes(M, N, K)
+    p_ws, n_ws, keep = _scratch(ws, n, dev, stream)
+    st = lib().lq_gated_linear_bwd(
+        _mat(dh, "dh", (M, N), dt, dev), _mat(g, "g", (M, N), dt, dev),
+        _mat(u, "u", (M, N), dt, dev), _mat(x, "x", (M, K), dt, dev),
+        _mat(wg, "wg", (N, K), dt, dev), _mat(wu, "wu", (N, K), dt, dev), _code(dh, "dh"), M, N,
+        K, act, _mat(dx, "dx", (M, K), dt, dev), _mat(dwg, "dwg", (N, K), g_dtype, dev),
+        _mat(dwu, "dwu", (N, K), g_dtype, dev), _mat(dbg, "dbg", (N,), g_dtype, dev),
+        _mat(dbu, "dbu", (N,), g_dtype, dev), _DTYPE_CODES.get(g_dtype, -1),
+        1 if accumulate else 0, p_ws, n_ws, _stream(stream))
+    _check(st, "lq_gated_linear_bwd")
+    return dx, dwg, dwu, dbg, dbu
+
+
+def lq_distill_loss(logits: torch.Tensor, t_values: torch.Tensor, t_index: torch.Tensor, *,
+                    t_lse: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                    temp: float = 1.0, want_grad: bool = False,
+                    loss: Optional[torch.Tensor] = None, grad: Optional[torch.Tensor] = None,
+                    stream=None):
+    """Weighted divergence of each row's student logits (M x V) from the teacher's
+    k listed logits (t_values, t_index: M x k, int32 or int64; an index outside
+    the vocabulary is no entry); with t_lse (the teacher's log-partition at this
+    temperature) what is not listed is one more class.  Returns (loss, grad):
+    M float32 values and, if wanted, d loss / d logits; grad=logits writes in place."""
+    dev = _on_device(logits, "logits", 2)
+    M, V = logits.shape
+    if t_index.dtype not in (torch.int32, torch.int64):
+        raise ValueError("t_index must be int32 or int64")
+    k = t_values.shape[-1]
+    if loss is None:
+        loss = _empty((M,), torch.float32, dev, stream)
+    if grad is None and want_grad:
+        grad = _empty((M, V), logits.dtype, dev, stream)
+    f32 = torch.float32
+    st = lib().lq_distill_loss(
+        _mat(logits, "logits", (M, V), logits.dtype, dev), _code(logits, "logits"), M, V,
+        _mat(t_values, "t_values", (M, k), t_values.dtype, dev), _code(t_values, "t_values"),
+        _mat(t_index, "t_index", (M, k), t_index.dtype, dev), t_index.element_size(), k,
+        _mat(t_lse, "t_lse", (M,), f32, dev), _mat(weight, "weight", (M,), f32, dev), float(temp),
+        _mat(loss, "loss", (M,), f32, dev), _mat(grad, "grad", (M, V), logits.dtype, dev),
+        _stream(stream))
+    _check(st, "lq_distill_loss")
+    return loss, grad
 
 
 LQ_NOALLOC_SCRATCH_BYTES = 16 << 20

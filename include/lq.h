@@ -61,6 +61,14 @@ typedef int32_t lq_status;
 /* element types of activation inputs */
 #define LQ_F32   0
 #define LQ_BF16  1
+#define LQ_F16   2  /* dense entry points and the distillation loss only */
+
+/* activations of the dense entry points */
+#define LQ_ACT_NONE      0
+#define LQ_ACT_RELU      1
+#define LQ_ACT_SILU      2  /* z / (1 + exp(-z)) */
+#define LQ_ACT_GELU      3  /* z Phi(z), Phi the normal distribution function */
+#define LQ_ACT_GELU_TANH 4  /* its tanh form */
 
 /* lq_loop_stack modes */
 #define LQ_OPEN  0  /* every (t, l) reads its own input                       */
@@ -322,6 +330,130 @@ int64_t lq_hessian_workspace_bytes(int64_t M, int64_t K, int32_t T);
 lq_status lq_trajectory_hessian(const void* d_X, int32_t x_dtype, int64_t M, int64_t K,
                                 int32_t T, float* d_H, int32_t accumulate, void* d_ws,
                                 int64_t ws_bytes, void* stream);
+
+/*
+ * Dense products of the modules that stay unquantized and of the unquantized
+ * block that calibration trains against ("paper_specification.yaml" of the
+ * LoopQ reproduction: the output head, embeddings and time/modulation modules
+ * stay unquantized; the trajectory objective runs an unquantized teacher next
+ * to the student).  The five entry points below share these rules:
+ *   - matrices of one element type `dtype`, LQ_BF16 or LQ_F16 (others
+ *     LQ_ERR_UNSUPPORTED); products are exact in float32 and summed in float32,
+ *     bias, activation, product and residual are applied in float32, and every
+ *     output is rounded once.
+ *   - x is M x K, a weight N x K, outputs M x N; K a multiple of 8
+ *     (LQ_ERR_SHAPE), M >= 0 and N >= 1 arbitrary, each below 2^31 - 256 and
+ *     no matrix above 2^46 elements.
+ *   - pointers are 16-byte aligned (LQ_ERR_ALIGN), the workspace 256-byte
+ *     aligned; an output must not overlap an input or another output
+ *     (LQ_ERR_ARG), except that the residual and the output may be the same
+ *     matrix.
+ *   - M == 0 is valid: nothing is read; weight and bias gradients become zero
+ *     (or stay as they are when accumulating).
+ * Asynchronous on `stream`; safe to capture.  Results do not depend on the
+ * workspace's contents, and two runs of a call give the same bits.
+ *
+ * lq_dense_linear -- y = act(x W^T + bias) + residual.
+ *   d_bias      N values, or NULL;  d_residual  M x N, or NULL;
+ *   d_y         out M x N;
+ *   d_z         out M x N, the pre-activation x W^T + bias that
+ *               lq_dense_linear_bwd reads, or NULL.
+ *   d_ws        lq_dense_linear_workspace_bytes(M, N, K) bytes (may be NULL
+ *               when that is 0).
+ */
+int64_t lq_dense_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+lq_status lq_dense_linear(const void* d_x, const void* d_w, const void* d_bias,
+                          const void* d_residual, int32_t dtype, int64_t M, int64_t N, int64_t K,
+                          int32_t act, void* d_y, void* d_z, void* d_ws, int64_t ws_bytes,
+                          void* stream);
+
+/*
+ * lq_dense_linear_bwd -- the gradients of lq_dense_linear:
+ *   dz = dy act'(z);  dx = dz W;  dw = dz^T x;  db = column sums of dz
+ * (the residual's gradient is dy).
+ *   d_z         the saved pre-activation M x N; NULL with LQ_ACT_NONE, where it
+ *               is not read.
+ *   d_dx M x K, d_dw N x K, d_db N: each may be NULL (not wanted); with one of
+ *   them NULL the inputs only it needs (W for dx, x for dw) may be NULL too.
+ *   g_dtype     element type of dw and db: dtype or LQ_F32.
+ *   accumulate  add to what dw and db hold (the gradient of a weight that all
+ *               loops share, loop by loop); needs g_dtype LQ_F32
+ *               (LQ_ERR_UNSUPPORTED).
+ * dz is rounded to dtype before the products (the tensor cores' operand
+ * type); db sums the float32 values.
+ */
+int64_t lq_dense_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t act);
+lq_status lq_dense_linear_bwd(const void* d_dy, const void* d_z, const void* d_x,
+                              const void* d_w, int32_t dtype, int64_t M, int64_t N, int64_t K,
+                              int32_t act, void* d_dx, void* d_dw, void* d_db, int32_t g_dtype,
+                              int32_t accumulate, void* d_ws, int64_t ws_bytes, void* stream);
+
+/*
+ * lq_gated_linear -- both projections of a gated feed-forward block, the
+ * activation and the product in one kernel:
+ *   g = x Wg^T + bias_g;  u = x Wu^T + bias_u;  h = act(g) u.
+ * The block's down projection with its residual is lq_dense_linear(h, Wd).
+ *   d_bias_g, d_bias_u  N values each, or NULL;
+ *   d_h         out M x N;
+ *   d_g, d_u    out M x N, what lq_gated_linear_bwd reads; both or neither.
+ */
+int64_t lq_gated_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
+lq_status lq_gated_linear(const void* d_x, const void* d_wg, const void* d_wu,
+                          const void* d_bias_g, const void* d_bias_u, int32_t dtype, int64_t M,
+                          int64_t N, int64_t K, int32_t act, void* d_h, void* d_g, void* d_u,
+                          void* d_ws, int64_t ws_bytes, void* stream);
+
+/*
+ * lq_gated_linear_bwd -- the gradients of lq_gated_linear:
+ *   dg = dh u act'(g);  du = dh act(g);
+ *   dx = dg Wg + du Wu;  dwg = dg^T x;  dwu = du^T x;  dbg, dbu column sums.
+ * Outputs, g_dtype, accumulate and NULL as in lq_dense_linear_bwd.
+ */
+int64_t lq_gated_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K);
+lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u,
+                              const void* d_x, const void* d_wg, const void* d_wu, int32_t dtype,
+                              int64_t M, int64_t N, int64_t K, int32_t act, void* d_dx,
+                              void* d_dwg, void* d_dwu, void* d_dbg, void* d_dbu,
+                              int32_t g_dtype, int32_t accumulate, void* d_ws, int64_t ws_bytes,
+                              void* stream);
+
+/*
+ * lq_distill_loss -- divergence of the student's distribution from a teacher
+ * known by its top logits, and the gradient of the student's logits
+ * ("paper_specification.yaml" of the LoopQ reproduction: trajectory
+ * calibration, joint KL at temperature 1 with the teacher's top 1000 logits).
+ * Row m has V student logits z and k listed teacher logits t_i at vocabulary
+ * indices v_i; q = softmax(z / temp).
+ *   d_t_lse NULL: p = softmax(t / temp) over the listed entries, R = 0;
+ *   d_t_lse given: the teacher's log-partition of row m, log sum exp(t / temp)
+ *       over its whole vocabulary; p_i = exp(t_i / temp - t_lse), and what is
+ *       not listed is one more class with mass R = max(0, 1 - sum p):
+ *   loss[m] = w[m] (sum_i p_i (log p_i - log q_{v_i}) + R (log R - log Q)),
+ *       Q the student's mass outside the list (the R term is left out where R
+ *       or Q is zero);
+ *   grad    = d loss[m] / d z.
+ *   d_logits    M x V, dtype LQ_F32, LQ_BF16 or LQ_F16; entries may be -inf
+ *               (masked vocabulary).  Rows start anywhere: V is arbitrary.
+ *   d_t_values  M x k, t_dtype any of the three types; -inf counts nothing.
+ *   d_t_index   M x k vocabulary indices, int32 (idx_bytes 4) or int64 (8).  An
+ *               index outside [0, V) is no entry (padding of a shorter list);
+ *               one that a row lists again counts at its first position.
+ *   d_weight    M row weights (upstream gradient, 1 / rows, 0 for padding), or
+ *               NULL for 1.  A row of weight 0, and without d_t_lse a row
+ *               without an entry, has loss 0 and gradient 0 whatever its
+ *               logits hold.
+ *   d_loss      out M float32;  d_grad  out M x V of dtype, or NULL; it may be
+ *               d_logits itself (in place), no other overlap.
+ * 1 <= k <= V; a row's logits are at most LQ_DISTILL_MAX_ROW_BYTES
+ * (LQ_ERR_SHAPE); temp > 0.  Sums are float32 over up to a few hundred values
+ * of a thread, float64 beyond.  Asynchronous on `stream`; safe to capture.
+ */
+#define LQ_DISTILL_MAX_ROW_BYTES (8ll * 192 * 1024)
+lq_status lq_distill_loss(const void* d_logits, int32_t dtype, int64_t M, int64_t V,
+                          const void* d_t_values, int32_t t_dtype, const void* d_t_index,
+                          int32_t idx_bytes, int64_t k, const float* d_t_lse,
+                          const float* d_weight, float temp, float* d_loss, void* d_grad,
+                          void* stream);
 
 /*
  * lq_loop_linear_noalloc -- lq_loop_linear for callers that cannot allocate
