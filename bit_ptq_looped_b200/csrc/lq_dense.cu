@@ -32,6 +32,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 
 #include "lq_dense.cuh"
@@ -45,16 +46,33 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait
 
 __device__ int g_dense_status = 0;
 
-// Bounded wait that ignores the abort flag (teardown: no copy or MMA of this
-// CTA is in flight when it exits).
-__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
-      atomicExch(&g_dense_status, (int)LQ_ERR_DEVICE_TIMEOUT);
-      return;
+// Bounded wait on an mbarrier phase: false once `limit_ns` have passed or the
+// CTA's abort flag is up (and raises it on a timeout, so that the other roles
+// stop too).  The clock is read once in 1024 polls.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023u) == 0) {
+      if (*abort) return false;
+      const uint64_t t = global_timer_ns();
+      if (t0 == 0) {
+        t0 = t;
+      } else if (t - t0 > kWaitLimitNs) {
+        *abort = 1;
+        atomicExch(&g_dense_status, (int)LQ_ERR_DEVICE_TIMEOUT);
+        return false;
+      }
     }
   }
+}
+
+// The same wait without the abort flag (teardown: no copy or MMA of this CTA is
+// in flight when it exits).
+__device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
+  int none = 0;
+  wait_bounded(bar, parity, &none);
 }
 
 // ---------------------------------------------------------------------------
@@ -199,14 +217,106 @@ __host__ __device__ constexpr uint32_t instr_desc(uint32_t fmt, bool a_mn, bool 
          ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
+// kPair: CTAs that share one MMA (1, or 2: the pair's first CTA issues for both)
+template <int kPair>
 __device__ __forceinline__ void umma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t acc) {
+  if (kPair == 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+// arrival on `bar` (the same offset in both CTAs of a pair) once every MMA
+// issued so far has completed
+template <int kPair>
+__device__ __forceinline__ void commit_all(uint32_t bar) {
+  if (kPair == 1)
+    umma_commit(bar);
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+template <int kPair>
+__device__ __forceinline__ void tmem_take(uint32_t dst_smem, uint32_t ncols) {
+  if (kPair == 1) {
+    tmem_alloc(dst_smem, ncols);
+    tmem_relinquish();
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+}
+template <int kPair>
+__device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t ncols) {
+  if (kPair == 1)
+    tmem_dealloc(taddr, ncols);
+  else
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
+}
+
+// a tile into this CTA's shared memory; the bytes count on `bar`, a shared::cluster
+// address that may belong to the pair's first CTA
+template <int kPair>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                          int c0, int c1) {
+  if (kPair == 1)
+    tma_load_2d(dst, map, bar, c0, c1);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+// one lane of a converged warp.  The roles that issue TMA copies and MMAs run
+// with the whole warp and let the elected lane issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
-      : "memory");
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// the same shared-memory offset in the pair's first CTA
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t saddr) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(0));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -238,7 +348,7 @@ struct GemmParams {
   uint16_t* aux2;  // the up factor u
 };
 
-template <int kBN, int kEpi>
+template <int kBN, int kPair, int kEpi>
 struct Cfg {
   static constexpr int kEpiWarps = kBN >= 128 ? 8 : 4;
   // columns an epilogue warp handles: its column half of the tile (of each
@@ -246,7 +356,8 @@ struct Cfg {
   static constexpr int kCols = kBN / (kEpiWarps / 4) / (kEpi == kEpiGated ? 2 : 1);
   // columns per shared-memory unit: 128-byte rows, or 64-byte ones
   static constexpr int kUnit = (kEpi == kEpiF32 || kCols < 64) ? 32 : 64;
-  static constexpr uint32_t kStageA = BM * BK * 2, kStageB = kBN * BK * 2;
+  // a CTA of a pair holds its own 128 rows of A and its half of B's rows
+  static constexpr uint32_t kStageA = BM * BK * 2, kStageB = kBN / kPair * BK * 2;
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
   static constexpr uint32_t kStaging = kEpiWarps * 32 * 128;
   static constexpr int kStages = (int)((226u * 1024u - 1024u - 512u - kStaging) / kStageBytes);
@@ -424,12 +535,12 @@ __device__ __forceinline__ void tile_at(int t, int tm, int tn, int& im, int& in)
   in = r / h;
 }
 
-template <typename T, int kBN, bool kAMn, bool kBMn, int kEpi>
-__global__ void __launch_bounds__(Cfg<kBN, kEpi>::kThreads, 1)
+template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi>
+__global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
     k_dense_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                  const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
                  const __grid_constant__ GemmParams P) {
-  using C = Cfg<kBN, kEpi>;
+  using C = Cfg<kBN, kPair, kEpi>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -443,8 +554,11 @@ __global__ void __launch_bounds__(Cfg<kBN, kEpi>::kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + C::kOffMisc + 4);
   constexpr int kTileN = kEpi == kEpiGated ? kBN / 2 : kBN;  // output columns of a tile
-  const int tm = (int)((P.M + BM - 1) / BM), tn = (int)((P.N + kTileN - 1) / kTileN);
+  constexpr int kTileM = BM * kPair;
+  const int tm = (int)((P.M + kTileM - 1) / kTileM), tn = (int)((P.N + kTileN - 1) / kTileN);
   const int n_tiles = tm * tn;
+  const int rank = kPair == 1 ? 0 : (int)cluster_rank();
+  const int t_first = blockIdx.x / kPair, t_step = gridDim.x / kPair;
 
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -454,98 +568,112 @@ __global__ void __launch_bounds__(Cfg<kBN, kEpi>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(bar_accf + 8 * b, 1);
-      mbar_init(bar_acce + 8 * b, C::kEpiWarps);
+      mbar_init(bar_acce + 8 * b, C::kEpiWarps * kPair);
     }
     mbar_init(bar_drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 0) {
-    tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
-    tmem_relinquish();
-  }
+  if (warp == 0) tmem_take<kPair>(smem_u32(tmem_slot), C::kTmemCols);
   tc_fence_before();
   __syncthreads();
+  if (kPair == 2) cluster_sync_all();  // both CTAs' barriers are set up
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // everything below reads or writes global memory
 
   if (warp == C::kEpiWarps) {
     // ---- TMA producer
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-        int im, in;
-        tile_at(t, tm, tn, im, in);
-        const int m0 = im * BM, n0 = in * kTileN;
-        for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
-          const int st = it % C::kStages;
-          if (!mbar_wait_bounded(bar_empty + 8 * st, ((uint32_t)(it / C::kStages) & 1u) ^ 1u,
-                                 abort_flag, &g_dense_status, kWaitLimitNs)) {
-            ok = false;
-            break;
-          }
-          const bool first = kb < P.n_kb1;
-          const CUtensorMap* a = first ? &tmA : &tmA2;
-          const CUtensorMap* b = first ? &tmB : &tmB2;
-          const int k0 = (first ? kb : kb - P.n_kb1) * BK;
-          const uint32_t full = bar_full + 8 * st;
-          const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
-          mbar_arrive_expect_tx(full, C::kStageBytes);
+    const bool leader = elect_one();
+    int it = 0, st = 0;
+    uint32_t ph = 1u;  // parity to wait for: the ring starts out empty
+    bool ok = true;
+    for (int t = t_first; t < n_tiles && ok; t += t_step) {
+      int im, in;
+      tile_at(t, tm, tn, im, in);
+      const int m0 = im * kTileM + rank * BM;
+      const int n0 = in * kTileN + (kEpi == kEpiGated ? 0 : rank * (kBN / kPair));
+      for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
+        if (!wait_bounded(bar_empty + 8 * st, ph, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const bool first = kb < P.n_kb1;
+        const CUtensorMap* a = first ? &tmA : &tmA2;
+        const CUtensorMap* b = first ? &tmB : &tmB2;
+        const int k0 = (first ? kb : kb - P.n_kb1) * BK;
+        // a stage is full once the bytes of both CTAs have arrived at the
+        // first one's barrier, where the MMAs are issued
+        const uint32_t full = kPair == 1 ? bar_full + 8 * st : in_first_cta(bar_full + 8 * st);
+        const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
+        if (leader) {
+          if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, C::kStageBytes * kPair);
           if (kAMn) {
 #pragma unroll
-            for (int c = 0; c < BM / 64; ++c) tma_load_2d(sa + c * 8192, a, full, m0 + 64 * c, k0);
+            for (int c = 0; c < BM / 64; ++c)
+              load_tile<kPair>(sa + c * 8192, a, full, m0 + 64 * c, k0);
           } else {
-            tma_load_2d(sa, a, full, k0, m0);
+            load_tile<kPair>(sa, a, full, k0, m0);
           }
           if (kBMn) {
 #pragma unroll
-            for (int c = 0; c < kBN / 64; ++c) tma_load_2d(sb + c * 8192, b, full, n0 + 64 * c, k0);
+            for (int c = 0; c < kBN / kPair / 64; ++c)
+              load_tile<kPair>(sb + c * 8192, b, full, n0 + 64 * c, k0);
+          } else if (kEpi == kEpiGated && kPair == 2) {
+            // the first CTA holds the gate's rows of B, the second the up ones
+            load_tile<kPair>(sb, rank == 0 ? &tmB : &tmB2, full, k0, n0);
           } else if (kEpi == kEpiGated) {
-            tma_load_2d(sb, &tmB, full, k0, n0);
-            tma_load_2d(sb + C::kStageB / 2, &tmB2, full, k0, n0);
+            load_tile<kPair>(sb, &tmB, full, k0, n0);
+            load_tile<kPair>(sb + C::kStageB / 2, &tmB2, full, k0, n0);
           } else {
-            tma_load_2d(sb, b, full, k0, n0);
+            load_tile<kPair>(sb, b, full, k0, n0);
           }
         }
+        __syncwarp();
+        if (++st == C::kStages) st = 0, ph ^= 1u;
       }
+    }
+    if (rank == 0)
       for (int i = max(0, it - C::kStages); i < it; ++i)
         wait_drain(bar_full + 8 * (i % C::kStages), (uint32_t)(i / C::kStages) & 1u);
-    }
   } else if (warp == C::kEpiWarps + 1) {
-    // ---- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = instr_desc(Elem<T>::kFormat, kAMn, kBMn, BM, kBN);
-      // bytes between consecutive 16-wide contraction steps of a stage
-      constexpr uint32_t stepA = kAMn ? 2048u : 32u, stepB = kBMn ? 2048u : 32u;
-      int it = 0, j = 0;
+    // ---- MMA issuer (of a pair: the first CTA's, for both)
+    if (rank == 0) {
+      constexpr uint32_t idesc = instr_desc(Elem<T>::kFormat, kAMn, kBMn, kTileM, kBN);
+      // descriptor units (16 bytes) between consecutive 16-wide contraction steps
+      constexpr uint64_t stepA = (kAMn ? 2048u : 32u) >> 4, stepB = (kBMn ? 2048u : 32u) >> 4;
+      const uint64_t descA = smem_desc(base, kAMn), descB = smem_desc(base + C::kOffB, kBMn);
+      const bool leader = elect_one();
+      int st = 0, j = 0;
+      uint32_t ph = 0u;
       bool ok = true;
-      for (int t = blockIdx.x; t < n_tiles && ok; t += gridDim.x, ++j) {
+      for (int t = t_first; t < n_tiles && ok; t += t_step, ++j) {
         const int buf = j & 1;
-        if (!mbar_wait_bounded(bar_acce + 8 * buf, ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag,
-                               &g_dense_status, kWaitLimitNs))
-          break;
+        if (!wait_bounded(bar_acce + 8 * buf, ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
-        for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
-          const int st = it % C::kStages;
-          if (!mbar_wait_bounded(bar_full + 8 * st, (uint32_t)(it / C::kStages) & 1u, abort_flag,
-                                 &g_dense_status, kWaitLimitNs)) {
+        for (int kb = 0; kb < P.n_kb; ++kb) {
+          if (!wait_bounded(bar_full + 8 * st, ph, abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
+          if (leader) {
+            const uint64_t da = descA + (uint64_t)(st * (C::kStageA >> 4));
+            const uint64_t db = descB + (uint64_t)(st * (C::kStageB >> 4));
 #pragma unroll
-          for (int i = 0; i < BK / 16; ++i)
-            umma_f16(d, smem_desc(sa + stepA * i, kAMn), smem_desc(sb + stepB * i, kBMn), idesc,
-                     (kb | i) ? 1u : 0u);
-          umma_commit(bar_empty + 8 * st);
+            for (int i = 0; i < BK / 16; ++i)
+              umma_f16<kPair>(d, da + stepA * i, db + stepB * i, idesc, (kb | i) ? 1u : 0u);
+            commit_all<kPair>(bar_empty + 8 * st);
+          }
+          __syncwarp();
+          if (++st == C::kStages) st = 0, ph ^= 1u;
         }
-        if (ok) umma_commit(bar_accf + 8 * buf);
+        if (ok && leader) commit_all<kPair>(bar_accf + 8 * buf);
+        __syncwarp();
       }
-      umma_commit(bar_drain);
+      if (leader) commit_all<kPair>(bar_drain);
+      __syncwarp();
       wait_drain(bar_drain, 0u);
     }
   } else {
@@ -554,15 +682,14 @@ __global__ void __launch_bounds__(Cfg<kBN, kEpi>::kThreads, 1)
     unsigned char* stg = gbase + C::kOffStaging + warp * 4096;
     constexpr int kRowBytes = C::kUnit * (kEpi == kEpiF32 ? 4 : 2);
     int j = 0;
-    for (int t = blockIdx.x; t < n_tiles; t += gridDim.x, ++j) {
+    for (int t = t_first; t < n_tiles; t += t_step, ++j) {
       int im, in;
       tile_at(t, tm, tn, im, in);
       const int buf = j & 1;
-      const int64_t row0 = (int64_t)im * BM + 32 * q;
+      const int64_t row0 = (int64_t)im * kTileM + rank * BM + 32 * q;
       const int64_t n0 = (int64_t)in * kTileN;
       const bool live = row0 < P.M;
-      if (!mbar_wait_bounded(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag,
-                             &g_dense_status, kWaitLimitNs))
+      if (!wait_bounded(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag))
         break;
       tc_fence_after();
       const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kBN);
@@ -650,14 +777,22 @@ __global__ void __launch_bounds__(Cfg<kBN, kEpi>::kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_acce + 8 * buf);
+      if (lane == 0) {
+        if (kPair == 1)
+          mbar_arrive(bar_acce + 8 * buf);
+        else
+          arrive_cluster(in_first_cta(bar_acce + 8 * buf));
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  // neither CTA leaves while the other's copies, MMAs or arrivals may still
+  // reach its shared memory
+  if (kPair == 2) cluster_sync_all();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, C::kTmemCols);
+    tmem_free<kPair>(tmem_base, C::kTmemCols);
   }
 }
 
@@ -959,39 +1094,73 @@ bool operand_map(CUtensorMap* m, const Operand& o, bool mn, bool bf16, int tile_
             : make_map(m, o.p, bf16, o.rows, o.k, o.ld, tile_rows);
 }
 
-template <typename T, int kBN, bool kAMn, bool kBMn, int kEpi>
+template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi>
 cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
                      const GemmParams& P, cudaStream_t s) {
-  using C = Cfg<kBN, kEpi>;
+  using C = Cfg<kBN, kPair, kEpi>;
   constexpr bool bf16 = Elem<T>::kFormat == 1;
-  constexpr int rowsB = kEpi == kEpiGated ? kBN / 2 : kBN;
+  constexpr int rowsB = kEpi == kEpiGated ? kBN / 2 : kBN / kPair;
   CUtensorMap mA, mA2, mB, mB2;
-  if (!operand_map(&mA, a, kAMn, bf16, BM) || !operand_map(&mA2, a2, kAMn, bf16, BM) ||
-      !operand_map(&mB, b, kBMn, bf16, rowsB) || !operand_map(&mB2, b2, kBMn, bf16, rowsB))
+  if (!operand_map(&mA, a, kAMn, bf16, BM) || !operand_map(&mB, b, kBMn, bf16, rowsB))
     return cudaErrorInvalidValue;
-  auto* k = k_dense_gemm<T, kBN, kAMn, kBMn, kEpi>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)C::kSmem);
+  mA2 = mA;
+  mB2 = mB;
+  if ((a2.p != a.p && !operand_map(&mA2, a2, kAMn, bf16, BM)) ||
+      (b2.p != b.p && !operand_map(&mB2, b2, kBMn, bf16, rowsB)))
+    return cudaErrorInvalidValue;
+  auto* k = k_dense_gemm<T, kBN, kPair, kAMn, kBMn, kEpi>;
+  static std::atomic<uint64_t> smem_set{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  constexpr int kTileN = kEpi == kEpiGated ? kBN / 2 : kBN;
-  const int64_t tiles = ((P.M + BM - 1) / BM) * ((P.N + kTileN - 1) / kTileN);
+  if (dev >= 64 || !((smem_set.load() >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) smem_set.fetch_or(1ull << dev);
+  }
+  constexpr int kTileN = kEpi == kEpiGated ? kBN / 2 : kBN, kTileM = BM * kPair;
+  const int64_t tiles = ((P.M + kTileM - 1) / kTileM) * ((P.N + kTileN - 1) / kTileN);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_kernel(k, dim3((unsigned)std::min<int64_t>(tiles, num_sms())), dim3(C::kThreads),
-                       C::kSmem, s, true, mA, mA2, mB, mB2, P);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, num_sms() / kPair) * kPair));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kPair;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = kPair == 1 ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, P);
 }
 
-// Tile width.  A wide tile reads fewer operand bytes per product, a narrow one
-// fills more SMs: take the widest whose tiles still cover the SMs, else the
-// narrowest.
+// Tile shape, by the time it would take.  Clocks of one 64-wide contraction
+// block: 512 for the 256 x 256 tile of a CTA pair (the tensor pipe's own time),
+// 330 for its 256 x 128 tile, 366 for a CTA's own 128 x 128 and 350 for its
+// 128 x 64 tile (what issuing the copies and MMAs takes); a tile's last
+// epilogue and a pair's handshakes come on top once.  Measured on
+// 2048 x 2048 x 5632: 35.6, 37.8, 43.1 and 71.7 us; on 16384 x 5632 x 2048:
+// 250, 320, 419 and 625; on 256 x 2048 x 2048: 15.7, 10.0, 10.4 and 9.9; on
+// 2048 x 256 x 256: 8.5, 5.3, 4.9 and 4.5.
 template <typename T, bool kAMn, bool kBMn, int kEpi>
 cudaError_t pick_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
                       const GemmParams& P, cudaStream_t s) {
   constexpr int f = kEpi == kEpiGated ? 2 : 1;
-  const int64_t tm = (P.M + BM - 1) / BM;
-  auto tiles = [&](int bn) { return tm * ((P.N * f + bn - 1) / bn); };
-  if (tiles(256) >= num_sms()) return run_gemm<T, 256, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
-  if (tiles(128) >= num_sms()) return run_gemm<T, 128, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
-  return run_gemm<T, 64, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  auto clocks = [&](int bm, int bn, int slots, int64_t per_block, int64_t once) {
+    const int64_t tiles = ((P.M + bm - 1) / bm) * ((P.N * f + bn - 1) / bn);
+    return (tiles + slots - 1) / slots * P.n_kb * per_block + once;
+  };
+  const int sms = num_sms();
+  const int64_t c2256 = clocks(256, 256, sms / 2, 512, 7800), c2128 = clocks(256, 128, sms / 2, 330, 4300),
+                c128 = clocks(128, 128, sms, 366, 3000), c64 = clocks(128, 64, sms, 350, 2600);
+  const int64_t best = std::min(std::min(c2256, c2128), std::min(c128, c64));
+  if (best == c2256) return run_gemm<T, 256, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  if (best == c2128) return run_gemm<T, 128, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  if (best == c128) return run_gemm<T, 128, 1, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  return run_gemm<T, 64, 1, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
 }
 
 GemmParams base_params(int64_t M, int64_t N, int64_t kdim) {

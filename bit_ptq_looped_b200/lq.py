@@ -132,8 +132,8 @@ def _dev(t: torch.Tensor, name: str) -> int:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: building a Stream object takes 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -468,18 +468,15 @@ def _code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _mat(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> Optional[int]:
+def _mat(t: Optional[torch.Tensor], name: str, shape, dtype, device: torch.device) -> Optional[int]:
     """Device pointer of a contiguous tensor of this shape and dtype on this device."""
     if t is None:
         return None
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (t.shape != shape or t.dtype != dtype or t.get_device() != device.index
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
+                         f"{device}, not {t.dtype} of shape {tuple(t.shape)} on {t.device}"
+                         + ("" if t.is_contiguous() else " with strides %s" % (t.stride(),)))
     return t.data_ptr()
 
 
@@ -531,8 +528,9 @@ def lq_dense_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
         y = _empty((M, N), dt, dev, stream)
     if z is None and want_z:
         z = _empty((M, N), dt, dev, stream)
-    p_ws, n_ws, keep = _scratch(ws, lib().lq_dense_linear_workspace_bytes(M, N, K), dev, stream)
-    st = lib().lq_dense_linear(
+    L = _lib or lib()
+    p_ws, n_ws, keep = _scratch(ws, L.lq_dense_linear_workspace_bytes(M, N, K), dev, stream)
+    st = L.lq_dense_linear(
         _mat(x, "x", (M, K), dt, dev), _mat(w, "w", (N, K), dt, dev),
         _mat(bias, "bias", (N,), dt, dev), _mat(residual, "residual", (M, N), dt, dev),
         _code(x, "x"), M, N, K, act, _mat(y, "y", (M, N), dt, dev),
