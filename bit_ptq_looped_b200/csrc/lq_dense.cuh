@@ -52,5 +52,6 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s);
 // the dense kernels' status word (LQ_ERR_DEVICE_TIMEOUT after a bounded wait
 // expired), read and cleared
 int take_dense_status();
+int take_distill_status();  // the distillation kernel's
 
 }  // namespace lq
