@@ -287,18 +287,6 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
         : "memory");
 }
 
-// one lane of a converged warp.  The roles that issue TMA copies and MMAs run
-// with the whole warp and let the elected lane issue.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));

@@ -6,6 +6,18 @@
 
 namespace lq {
 
+// one lane of a converged warp.  The roles that issue TMA copies and MMAs run
+// with the whole warp and let the elected lane issue.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 constexpr int64_t kDenseRowsMax = 16;  // rows up to which the weight-streaming kernel runs
 
 // y = act(x w^T + bias) + res, or with w2 y = act(x w^T + bias) * (x w2^T + bias2);
@@ -52,6 +64,5 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s);
 // the dense kernels' status word (LQ_ERR_DEVICE_TIMEOUT after a bounded wait
 // expired), read and cleared
 int take_dense_status();
-int take_distill_status();  // the distillation kernel's
 
 }  // namespace lq

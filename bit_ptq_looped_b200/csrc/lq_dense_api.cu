@@ -336,9 +336,9 @@ lq_status lq_distill_loss(const void* d_logits, int32_t dtype, int64_t M, int64_
     return LQ_ERR_ARG;
   }
   const int64_t esz = dtype == LQ_F32 ? 4 : 2, tsz = t_dtype == LQ_F32 ? 4 : 2;
-  if (k > V || V > LQ_DISTILL_MAX_ROW_BYTES / esz) {
-    set_error("V=%lld, k=%lld: k must not exceed V, nor a row's logits %lld bytes", (long long)V,
-              (long long)k, (long long)LQ_DISTILL_MAX_ROW_BYTES);
+  if (k > V || k > LQ_DISTILL_MAX_K || V > LQ_DISTILL_MAX_V) {
+    set_error("V=%lld, k=%lld: k must not exceed V nor %d, and V not %d", (long long)V,
+              (long long)k, LQ_DISTILL_MAX_K, LQ_DISTILL_MAX_V);
     return LQ_ERR_SHAPE;
   }
   if (M > kMaxExtent / 8 || M * V > kMaxElems) {

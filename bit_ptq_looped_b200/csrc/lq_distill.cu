@@ -14,20 +14,26 @@
 // a difference, which loses everything when the listed entries hold nearly
 // all of the student's mass).
 //
-// What bounds it is memory: each logit is read once and each gradient written
-// once.  A row (or, over a cluster of 2, 4 or 8 CTAs, an equal slice of it) is
-// brought to shared memory by one bulk copy, reduced there (maximum, sum), the
-// few numbers of the slices are exchanged through distributed shared memory,
-// the gradient replaces the logits in place, the listed entries' gradients are
-// put over it, and one bulk copy writes the slice back.  Next to memory it is
-// the exponential unit (two exponentials per logit, 16 per clock and SM) that
-// sets the pace; the passes therefore use packed maxima, two-lane float32
-// arithmetic and nothing per element that could be done per row.
+// What bounds it is memory, each logit read once and each gradient written
+// once, and next to it the exponential unit (two exponentials per logit, 16 per
+// clock and SM).  A CTA, or over a cluster of 2, 4 or 8 CTAs each one, walks its
+// columns twice: a first pass with a running maximum and sum, and for the
+// gradient a second one that finds the row in L2, where the rows in flight (some
+// 100 KB each, four per SM) stay; the gradients are stored as streaming data so
+// as not to displace them.  Nothing limits the row's length, and nothing waits
+// but at barriers.  Measured, 8192 x 49152 bf16 logits: 219 us for the loss
+// (floor 123), 372 with the gradient (floor 246).  Holding the row in shared
+// memory between the passes (bulk copies in and out, two rows per SM) took 250
+// and 342-365, and 46-56 against 26 for the loss of 255 x 100003 float32 logits;
+// a ring of bulk copies running ahead across passes and rows took 600, and keeping
+// part of the row in shared memory 555: what shared memory takes, the L1 lines
+// of the loads in flight lack.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "lq_dense.cuh"
 
@@ -36,11 +42,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
-constexpr int kKeep = 2;  // listed entries a thread keeps in registers
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxSmem = 164 * 1024;  // 64 KB of bitmap, 96 KB of listed entries
+constexpr int kUnroll = 4;  // 16-byte loads of a thread's batch
+constexpr int kBigThreads = 256;
 constexpr int kMaxCluster = 8;
+constexpr size_t kSmallSlice = 32 * 1024;  // bytes of a slice up to which 128 threads take it
 constexpr float kNegInf = -INFINITY;
 
 template <typename T>
@@ -57,6 +63,9 @@ struct Log<float> {
   static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
     return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
                       __float_as_uint(f[3]));
+  }
+  static __device__ __forceinline__ uint4 nothing() {  // -inf throughout
+    return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
   }
   // running maximum of 16-byte vectors, in the type's own pairs
   using Run = float;
@@ -88,6 +97,9 @@ struct Log<__nv_bfloat16> {
       q[i] = *reinterpret_cast<uint32_t*>(&v);
     }
     return make_uint4(q[0], q[1], q[2], q[3]);
+  }
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
   }
   using Run = __nv_bfloat162;
   static __device__ __forceinline__ Run run_start() { return __float2bfloat162_rn(kNegInf); }
@@ -122,6 +134,9 @@ struct Log<__half> {
     }
     return make_uint4(q[0], q[1], q[2], q[3]);
   }
+  static __device__ __forceinline__ uint4 nothing() {
+    return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
+  }
   using Run = __half2;
   static __device__ __forceinline__ Run run_start() { return __float2half2_rn(kNegInf); }
   static __device__ __forceinline__ Run run_max(Run m, const uint4& w) {
@@ -139,8 +154,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ int g_distill_status = 0;
-
 struct DistillParams {
   const void* z;
   void* grad;
@@ -149,9 +162,9 @@ struct DistillParams {
   const float* t_lse;
   const float* weight;
   float* loss;
-  int64_t V;
+  int64_t M, V;
   int k, t_dtype, idx64;
-  int slice;  // elements per CTA, a multiple of 32
+  int slice;   // elements per CTA, a multiple of 32
   float temp, inv_temp;
   double c2d;  // log2(e) / temp
   float c2;    // the same, rounded: the student's exponents, and consistently its
@@ -172,7 +185,8 @@ __device__ __forceinline__ float warp_max(float v) {
   for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
   return v;
 }
-__device__ __forceinline__ double warp_sum(double v) {
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
@@ -180,29 +194,32 @@ __device__ __forceinline__ double warp_sum(double v) {
 
 // what a slice tells the others
 struct Part {
-  float m, tm;       // maximum of its logits, of its teacher entries
-  double s, top;     // sum over its logits (rest class: those not listed), listed ones
-  double ts;         // sum over its teacher entries (rest class: of p)
+  float m, m2nd;     // maximum of its logits; of its teacher entries (rest class: listed logits)
+  double s, s2nd;    // the sums of exponentials that go with them (rest class: s over
+                     // those not listed)
+  double p_sum;      // rest class: sum of p
 };
-// a row's numbers, worked out by one thread
+// a row's numbers, worked out by one thread.  What the gradient waits for needs
+// divisions only; the logarithms come at the end, for the loss alone.
 struct RowNumbers {
   float m2;      // exponents are z c2 - m2
   float f_rest;  // gradient of an entry that is not listed, over its exponential
   float f_top;   // C / S times the scale, the same for listed entries
-  double p_sub;  // log2 of a listed p is t c2 - p_sub
-  double q_sub;  // log2 q is z c2 - q_sub
-  int has_p;     // the listed entries carry mass
-  double tail;   // the rest class's share of the loss
+  float inv_ts;  // no rest class: one over the listed exponentials' sum, 0 if there is none
+  float tm2;     // exponents of p are t c2 - tm2 (no rest class)
 };
 
-__device__ __forceinline__ void block_max2(float& a, float& b, float* sm) {
-  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
-  a = warp_max(a);
-  b = warp_max(b);
-  if (l == 0) sm[w] = a, sm[kWarps + w] = b;
-  __syncthreads();
-  a = warp_max(sm[l % kWarps]);
-  b = warp_max(sm[kWarps + l % kWarps]);
+// Running maximum and sum of exponentials: s counts in units of 2^m2, m2 = m c2
+// rounded (never contracted into a multiply-add, or two sums with the same
+// maximum would count in different units).
+struct Run1 {
+  float m, m2, s;
+};
+// the two as one, in a fixed order of lanes
+__device__ __forceinline__ Run1 warp_join(Run1 r, float c2) {
+  const float m = warp_max(r.m), m2 = m == kNegInf ? 0.f : __fmul_rn(m, c2);
+  const float s = warp_sum(r.m == kNegInf ? 0.f : r.s * ex2(r.m2 - m2));
+  return {m, m2, s};
 }
 
 // log2 p of a listed entry, in float64: logit and log-partition may be far larger
@@ -211,113 +228,140 @@ __device__ __forceinline__ double log2p(float t, double c2d, double lse2) {
   return (double)t * c2d - lse2;
 }
 
-template <typename T, bool kTail>
-__global__ void __launch_bounds__(kThreads, 2) k_distill(const DistillParams P) {
-  constexpr int kE = Log<T>::kE;
-  extern __shared__ __align__(128) unsigned char smem[];
+// What a CTA holds of one row: its slice of the columns, counted from the
+// 16-byte boundary at or before the row's start (column j of the row is
+// j + lead), so that the slice's vectors are aligned in global memory.
+template <typename T>
+struct Slice {
+  static constexpr int kE = Log<T>::kE;
+  int64_t c0;      // row column of slice element 0
+  int lo, hi;      // valid slice elements
+  int v_lo, v_hi;  // whole 16-byte vectors
+  int edge0, n_edge;
+  __device__ __forceinline__ Slice(const void* z, int64_t row, int64_t V, int rank, int slice) {
+    const int lead = (int)(((uintptr_t)z / sizeof(T) + (uint64_t)(row * V)) % kE);
+    c0 = (int64_t)rank * slice - lead;
+    lo = (int)(c0 < 0 ? -c0 : 0);
+    const int64_t left = V - c0;
+    hi = (int)(left < 0 ? 0 : left < slice ? left : slice);
+    v_lo = (lo + kE - 1) / kE;
+    v_hi = max(v_lo, hi / kE);
+    // the few elements before and after the vectors
+    edge0 = max(0, min(hi, v_lo * kE) - lo);
+    n_edge = edge0 + max(0, hi - v_hi * kE);
+  }
+  // slice element of edge number i < n_edge
+  __device__ __forceinline__ int edge(int i) const {
+    return i < edge0 ? lo + i : v_hi * kE + (i - edge0);
+  }
+};
+
+template <typename T, bool kTail, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+    k_distill(const __grid_constant__ DistillParams P) {
+  constexpr int kE = Log<T>::kE, kWarps = kThreads / 32;
+  extern __shared__ uint32_t bits[];  // the slice's listed entries
+  // the listed entries, each read and written by one thread: position in the
+  // slice (-1 for none of it), teacher logit, student logit
+  int* ent_e = reinterpret_cast<int*>(bits + P.slice / 32);
+  float* ent_t = reinterpret_cast<float*>(ent_e + P.k);
+  float* ent_z = ent_t + P.k;
   __shared__ Part parts[kMaxCluster];
   __shared__ double loss_parts[kMaxCluster];
-  __shared__ double sm_d[3][kWarps];
-  __shared__ float sm_f[2 * kWarps];
+  __shared__ float sm_m[2][32], sm_s[2][32];
+  __shared__ double sm_d[2][32];
   __shared__ RowNumbers row_n;
-  __shared__ __align__(8) unsigned long long bar;
   __shared__ int flags;  // 1: an entry is in range, 2: an index is listed again
   cg::cluster_group cluster = cg::this_cluster();
   const int n_parts = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int64_t row = blockIdx.x / n_parts;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  T* zs = reinterpret_cast<T*>(smem);
-  uint32_t* bits = reinterpret_cast<uint32_t*>(smem + (size_t)P.slice * sizeof(T));
 
   pdl_trigger();
-  if (tid == 0) {
-    mbar_init(smem_u32(&bar), 1);
-    fence_mbar_init();
-    flags = 0;
-  }
+  if (tid == 0) flags = 0;
   for (int i = tid; i < P.slice / 32; i += kThreads) bits[i] = 0u;
+  const Slice<T> sl(P.z, row, P.V, rank, P.slice);
+  const T* zs = (const T*)P.z + row * P.V + sl.c0;  // slice element 0
+  T* gs = P.grad ? (T*)P.grad + row * P.V + sl.c0 : nullptr;
+  const uint4* vec = reinterpret_cast<const uint4*>(zs);
+  const int64_t list = row * P.k;
+  // Both passes walk the vectors in batches of kUnroll per thread, the next batch
+  // on its way while one is worked on.  The last batch may be partial: what lies
+  // beyond the end is -inf, which counts nothing.
+  const int n_vec = sl.v_hi - sl.v_lo, n_full = n_vec / (kUnroll * kThreads);
+  const int n_batch = (n_vec + kUnroll * kThreads - 1) / (kUnroll * kThreads);
+  vec += sl.v_lo + tid;
+  auto batch = [&](uint4 (&x)[kUnroll], int b) {
+    const uint4* p = vec + b * (kUnroll * kThreads);
+    if (b < n_full) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) x[u] = p[u * kThreads];
+    } else {
+      const int left = n_vec - tid - b * (kUnroll * kThreads);
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) x[u] = u * kThreads < left ? p[u * kThreads] : Log<T>::nothing();
+    }
+  };
   pdl_wait();
-  __syncthreads();
+  // the row's weight, its first batch and its list travel together
   const float w = P.weight ? P.weight[row] : 1.f;
-  // columns are counted from the 16-byte boundary at or before the row's
-  // start: column j of the row is j + lead; this slice holds [c0, c0 + slice)
-  const T* zrow = (const T*)P.z + row * P.V;
-  T* grow = P.grad ? (T*)P.grad + row * P.V : nullptr;
-  const int lead = (int)(((uintptr_t)zrow & 15u) / sizeof(T));
-  const int64_t c0 = (int64_t)rank * P.slice - lead;  // row column of slice element 0
-  const int lo = (int)(c0 < 0 ? -c0 : 0);             // first valid slice element
-  const int64_t left = P.V - c0;
-  const int hi = (int)(left < 0 ? 0 : left < P.slice ? left : P.slice);  // end of the valid ones
-  // whole 16-byte vectors, and the few elements before and after them
-  const int v_lo = (lo + kE - 1) / kE, v_hi = max(v_lo, hi / kE);
-  const int edge0 = min(hi, v_lo * kE) - lo, edge1 = max(0, hi - v_hi * kE);
-  // element of edge number i < edge0 + edge1
-  auto edge_at = [&](int i) { return i < edge0 ? lo + i : v_hi * kE + (i - edge0); };
-  const int n_edge = max(0, edge0) + (v_hi * kE < hi ? edge1 : 0);
-
+  uint4 x[kUnroll];
+  batch(x, 0);
+  bool any = false;
+  for (int i0 = tid; i0 < P.k; i0 += 4 * kThreads) {
+    int64_t v[4];
+    float t[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kThreads;
+      v[j] = i < P.k ? index_at(P, list + i) : -1;
+      t[j] = i < P.k ? teacher_at(P, list + i) : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i >= P.k) break;
+      const int64_t e = v[j] - sl.c0;
+      const bool in = v[j] >= 0 && v[j] < P.V;
+      any |= in;
+      ent_e[i] = in && e >= sl.lo && e < sl.hi ? (int)e : -1;
+      ent_t[i] = t[j];
+    }
+  }
   auto zero_row = [&]() {
     if (rank == 0 && tid == 0) P.loss[row] = 0.f;
-    if (!grow) return;
-    for (int v = v_lo + tid; v < v_hi; v += kThreads)
-      *reinterpret_cast<uint4*>(grow + c0 + (int64_t)v * kE) = make_uint4(0, 0, 0, 0);
-    if (tid < n_edge) Log<T>::put(grow + c0 + edge_at(tid), 0.f);
+    if (!gs) return;
+    for (int v = sl.v_lo + tid; v < sl.v_hi; v += kThreads)
+      reinterpret_cast<uint4*>(gs)[v] = make_uint4(0, 0, 0, 0);
+    if (tid < sl.n_edge) Log<T>::put(gs + sl.edge(tid), 0.f);
   };
-  // a row of weight 0 counts nothing, whatever its logits hold
+  // a row of weight 0 counts nothing, whatever its logits hold (the same
+  // decision in every CTA of the cluster)
   if (w == 0.f) {
-    zero_row();  // the same decision in every CTA of the cluster
+    zero_row();
     return;
   }
   if (n_parts > 1) cluster.barrier_arrive();  // this CTA runs: its shared memory may be written
-  const uint32_t bar_a = smem_u32(&bar);
-  const uint32_t copy_bytes = (uint32_t)(v_hi - v_lo) * 16u;
-  if (tid == 0 && copy_bytes) {
-    mbar_arrive_expect_tx(bar_a, copy_bytes);
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-            "r"(smem_u32(zs + v_lo * kE)),
-        "l"(zrow + c0 + (int64_t)v_lo * kE), "r"(copy_bytes), "r"(bar_a)
-        : "memory");
-  }
-  if (tid < n_edge) zs[edge_at(tid)] = zrow[c0 + edge_at(tid)];
+  __syncthreads();
 
-  // While the row travels: the listed entries.  Those of this slice are marked
-  // in a bitmap; a thread keeps its first ones (position in the slice, -1 for
-  // none, and teacher logit).
-  const int64_t list = row * P.k;
-  auto slice_pos = [&](int i, bool& valid) -> int {
-    const int64_t v = index_at(P, list + i);
-    const int64_t e = v - c0;
-    valid = v >= 0 && v < P.V;
-    return valid && e >= lo && e < hi ? (int)e : -1;
-  };
-  int keep_e[kKeep];
-  float keep_t[kKeep];
-  bool any = false, dup = false;
+  // mark the listed entries of the slice; an index that is listed again counts
+  // at its first position only
+  bool dup = false;
+  for (int i0 = tid; i0 < P.k; i0 += 4 * kThreads) {
+    float z[4];
+    int e[4];
 #pragma unroll
-  for (int r = 0; r < kKeep; ++r) {
-    const int i = tid + r * kThreads;
-    keep_e[r] = -1;
-    keep_t[r] = 0.f;
-    if (i < P.k) {
-      bool ok;
-      keep_e[r] = slice_pos(i, ok);
-      keep_t[r] = teacher_at(P, list + i);
-      any |= ok;
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + j * kThreads;
+      e[j] = i < P.k ? ent_e[i] : -1;
+      z[j] = e[j] >= 0 ? Log<T>::get(zs + e[j]) : 0.f;
     }
-  }
 #pragma unroll
-  for (int r = 0; r < kKeep; ++r)
-    if (keep_e[r] >= 0) {
-      const uint32_t b = 1u << (keep_e[r] & 31);
-      dup |= (atomicOr(&bits[keep_e[r] >> 5], b) & b) != 0;
-    }
-  for (int i = tid + kKeep * kThreads; i < P.k; i += kThreads) {
-    bool ok;
-    const int e = slice_pos(i, ok);
-    any |= ok;
-    if (e >= 0) {
-      const uint32_t b = 1u << (e & 31);
-      dup |= (atomicOr(&bits[e >> 5], b) & b) != 0;
+    for (int j = 0; j < 4; ++j) {
+      if (e[j] < 0) continue;
+      const uint32_t b = 1u << (e[j] & 31);
+      dup |= (atomicOr(&bits[e[j] >> 5], b) & b) != 0;
+      ent_z[i0 + j * kThreads] = z[j];
     }
   }
   any = __any_sync(~0u, any);
@@ -325,154 +369,153 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill(const DistillParams P) 
   if (lane == 0 && (any || dup)) atomicOr(&flags, (any ? 1 : 0) | (dup ? 2 : 0));
   __syncthreads();
   any = flags & 1;
-  dup = flags & 2;
-  // an index that is listed again counts at its first position only
-  auto first_of = [&](int i) {
-    const int64_t v = index_at(P, list + i);
-    for (int j = 0; j < i; ++j)
-      if (index_at(P, list + j) == v) return false;
-    return true;
-  };
-  if (dup) {
-#pragma unroll
-    for (int r = 0; r < kKeep; ++r)
-      if (keep_e[r] >= 0 && !first_of(tid + r * kThreads)) keep_e[r] = -1;
+  if (flags & 2) {
+    for (int i = tid; i < P.k; i += kThreads) {
+      const int64_t v = index_at(P, list + i);
+      bool first = true;
+      for (int j = 0; j < i && first; ++j) first = index_at(P, list + j) != v;
+      if (!first) ent_e[i] = -1;
+    }
   }
-  // fn(position, teacher logit) for this thread's entries of the slice
+  // fn(position, teacher logit, student logit) for this thread's entries
   auto for_entries = [&](auto&& fn) {
-#pragma unroll
-    for (int r = 0; r < kKeep; ++r)
-      if (keep_e[r] >= 0) fn(keep_e[r], keep_t[r]);
-    for (int i = tid + kKeep * kThreads; i < P.k; i += kThreads) {
-      bool ok;
-      const int e = slice_pos(i, ok);
-      if (e >= 0 && (!dup || first_of(i))) fn(e, teacher_at(P, list + i));
+    for (int i = tid; i < P.k; i += kThreads) {
+      const int e = ent_e[i];
+      if (e >= 0) fn(e, ent_t[i], ent_z[i]);
     }
   };
-  float tm = kNegInf;
-  if (!kTail) for_entries([&](int, float t) { tm = fmaxf(tm, t); });
+  auto marked = [&](int e) { return (bits[e >> 5] >> (e & 31)) & 1u; };
 
-  // the row has arrived
-  if (copy_bytes) {
-    if (!mbar_try_wait(bar_a, 0u)) {
-      uint64_t t0 = 0;
-      for (uint32_t i = 1; !mbar_try_wait(bar_a, 0u); ++i) {
-        if (i & 1023u) continue;
-        const uint64_t t = global_timer_ns();
-        if (t0 == 0) t0 = t;
-        // recorded for lq_check_device; the CTA goes on (to its cluster's
-        // barriers), with whatever has arrived
-        if (t - t0 > kWaitLimitNs) {
-          atomicExch(&g_distill_status, (int)LQ_ERR_DEVICE_TIMEOUT);
-          break;
-        }
+  // First pass: running maximum and sum; base-2 exponents are z c2 - m2.  A
+  // batch first raises the maximum (packed), then adds its exponentials.
+  Run1 r1 = {kNegInf, 0.f, 0.f};
+  float2 s2 = make_float2(0.f, 0.f);
+  const float2 c2v = make_float2(P.c2, P.c2);
+  auto raise = [&](float to) {
+    if (to > r1.m) {
+      const float n2 = __fmul_rn(to, P.c2), f = r1.m == kNegInf ? 0.f : ex2(r1.m2 - n2);
+      s2 = fmul2(s2, make_float2(f, f));
+      r1.m = to;
+      r1.m2 = n2;
+    }
+  };
+
+  for (int b = 0; b < n_batch; ++b) {
+    uint4 y[kUnroll];
+    if (b + 1 < n_batch) batch(y, b + 1);
+    typename Log<T>::Run run = Log<T>::run_start();
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) run = Log<T>::run_max(run, x[u]);
+    raise(Log<T>::run_end(run));
+    const float2 nm2 = make_float2(-r1.m2, -r1.m2);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      float f[kE];
+      Log<T>::unpack(x[u], f);
+      if (kTail) {
+        const int e = min(sl.v_lo + tid + (b * kUnroll + u) * kThreads, sl.v_hi - 1) * kE;
+        const uint32_t marks = bits[e >> 5] >> (e & 31);
+#pragma unroll
+        for (int i = 0; i < kE; ++i)
+          if ((marks >> i) & 1u) f[i] = kNegInf;
+      }
+#pragma unroll
+      for (int i = 0; i < kE; i += 2) {
+        const float2 q = ffma2(make_float2(f[i], f[i + 1]), c2v, nm2);
+        s2 = fadd2(s2, make_float2(ex2(q.x), ex2(q.y)));
       }
     }
-  }
-
-  // maxima
-  uint4* vec = reinterpret_cast<uint4*>(zs);
-  typename Log<T>::Run run = Log<T>::run_start();
-  for (int v = v_lo + tid; v < v_hi; v += kThreads) run = Log<T>::run_max(run, vec[v]);
-  float m = Log<T>::run_end(run);
-  if (tid < n_edge) m = fmaxf(m, Log<T>::get(zs + edge_at(tid)));
-  block_max2(m, tm, sm_f);
-
-  // sums, relative to the slice's maxima; base-2 exponents z c2 - m2
-  const float m2 = m == kNegInf ? 0.f : m * P.c2;
-  const float2 c2v = make_float2(P.c2, P.c2), nm2 = make_float2(-m2, -m2);
-  float2 s2 = make_float2(0.f, 0.f);
-  for (int v = v_lo + tid; v < v_hi; v += kThreads) {
-    float f[kE];
-    Log<T>::unpack(vec[v], f);
-    if (kTail) {
-      const uint32_t mark = bits[(v * kE) >> 5] >> ((v * kE) & 31);
 #pragma unroll
-      for (int i = 0; i < kE; ++i)
-        if ((mark >> i) & 1u) f[i] = kNegInf;
-    }
-#pragma unroll
-    for (int i = 0; i < kE; i += 2) {
-      const float2 x = ffma2(make_float2(f[i], f[i + 1]), c2v, nm2);
-      s2 = fadd2(s2, make_float2(ex2(x.x), ex2(x.y)));
-    }
+    for (int u = 0; u < kUnroll; ++u) x[u] = y[u];
   }
-  float s = s2.x + s2.y;
-  if (tid < n_edge) {
-    const int e = edge_at(tid);
-    if (!kTail || !((bits[e >> 5] >> (e & 31)) & 1u))
-      s += ex2(fmaf(Log<T>::get(zs + e), P.c2, -m2));
+  float z_edge = 0.f;
+  if (tid < sl.n_edge) {
+    z_edge = Log<T>::get(zs + sl.edge(tid));
+    raise(z_edge);
+    if (!kTail || !marked(sl.edge(tid))) s2.x += ex2(fmaf(z_edge, P.c2, -r1.m2));
   }
-  float top = 0.f, ts = 0.f;
+  if (gs) batch(x, 0);  // the second pass's first batch
+  r1.s = s2.x + s2.y;
+  // the listed entries: their teacher's maximum and sum, or with a rest class
+  // their student's exponentials, and the sum of p in float64 (1 - sum p may be
+  // small)
+  Run1 r2 = {kNegInf, 0.f, 0.f};
+  double p_sum = 0.0;
   const double lse2_t = kTail ? (double)P.t_lse[row] * 1.4426950408889634 : 0.0;
-  for_entries([&](int e, float t) {
-    if (kTail) {
-      top += ex2(fmaf(Log<T>::get(zs + e), P.c2, -m2));
-      ts += ex2((float)log2p(t, P.c2d, lse2_t));
-    } else if (tm != kNegInf) {
-      ts += ex2((t - tm) * P.c2);
+  for_entries([&](int, float t, float z) {
+    const float l = kTail ? z : t;
+    if (l > r2.m) {
+      const float n2 = __fmul_rn(l, P.c2);
+      r2.s = r2.m == kNegInf ? 0.f : r2.s * ex2(r2.m2 - n2);
+      r2.m = l;
+      r2.m2 = n2;
     }
+    r2.s += ex2(fmaf(l, P.c2, -r2.m2));
+    if (kTail) p_sum += (double)ex2((float)log2p(t, P.c2d, lse2_t));
   });
-  {
-    const double sd = warp_sum((double)s), td = warp_sum((double)ts);
-    const double pd = kTail ? warp_sum((double)top) : 0.0;
-    if (lane == 0) sm_d[0][warp] = sd, sm_d[1][warp] = td, sm_d[2][warp] = pd;
+  r1 = warp_join(r1, P.c2);
+  r2 = warp_join(r2, P.c2);
+  if (kTail) p_sum = warp_sum(p_sum);
+  if (lane == 0) {
+    sm_m[0][warp] = r1.m, sm_s[0][warp] = r1.s;
+    sm_m[1][warp] = r2.m, sm_s[1][warp] = r2.s;
+    if (kTail) sm_d[0][warp] = p_sum;
   }
   __syncthreads();
   if (n_parts > 1) cluster.barrier_wait();
   if (warp == 0) {
-    const double sd = warp_sum(lane < kWarps ? sm_d[0][lane] : 0.0);
-    const double td = warp_sum(lane < kWarps ? sm_d[1][lane] : 0.0);
-    const double pd = kTail ? warp_sum(lane < kWarps ? sm_d[2][lane] : 0.0) : 0.0;
-    if (lane < n_parts) {
-      Part* dst = n_parts > 1 ? cluster.map_shared_rank(&parts[rank], lane) : &parts[0];
-      dst->m = m;
-      dst->tm = tm;
-      dst->s = sd;
-      dst->top = pd;
-      dst->ts = td;
+    Part p;
+    double d[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float m = lane < kWarps ? sm_m[j][lane] : kNegInf, mm = warp_max(m);
+      const float f = m == kNegInf ? 0.f : ex2(__fmul_rn(m, P.c2) - __fmul_rn(mm, P.c2));
+      d[j] = warp_sum(m == kNegInf ? 0.0 : (double)(sm_s[j][lane] * f));
+      (j ? p.m2nd : p.m) = mm;
     }
+    p.s = d[0];
+    p.s2nd = d[1];
+    p.p_sum = kTail ? warp_sum(lane < kWarps ? sm_d[0][lane] : 0.0) : 0.0;
+    if (lane < n_parts)
+      *(n_parts > 1 ? cluster.map_shared_rank(&parts[rank], lane) : &parts[0]) = p;
+    __syncwarp();
   }
-  if (n_parts > 1)
-    cluster.sync();
-  else
-    __syncthreads();
+  if (n_parts > 1) cluster.sync();
 
   // the row's numbers, from the slices in order
+  double S = 0.0, total = 0.0, TS = 0.0, R = 0.0;
   if (tid == 0) {
-    float M = kNegInf, TM = kNegInf;
+    float M = kNegInf, M2nd = kNegInf;
     for (int r = 0; r < n_parts; ++r) {
       M = fmaxf(M, parts[r].m);
-      TM = fmaxf(TM, parts[r].tm);
+      M2nd = fmaxf(M2nd, parts[r].m2nd);
     }
-    const float M2 = M == kNegInf ? 0.f : M * P.c2;
-    double S = 0.0, Top = 0.0, TS = 0.0;
+    // exponents of listed logits are never above the row's own maximum
+    const float M2 = M == kNegInf ? 0.f : __fmul_rn(M, P.c2);
+    const float N2 = kTail ? M2 : M2nd == kNegInf ? 0.f : __fmul_rn(M2nd, P.c2);
+    auto scaled = [&](float m, double v, float to2) {
+      if (m == kNegInf) return 0.0;
+      const float d = __fmul_rn(m, P.c2) - to2;
+      return d == 0.f ? v : v * exp2((double)d);
+    };
+    double second = 0.0;
     for (int r = 0; r < n_parts; ++r) {
-      const Part& q = parts[r];
-      const double f = q.m == M ? 1.0 : q.m == kNegInf ? 0.0 : exp2((double)(q.m * P.c2) - M2);
-      S += q.s * f;
-      Top += q.top * f;
-      TS += kTail          ? q.ts
-            : q.tm == TM   ? q.ts
-            : q.tm == kNegInf ? 0.0
-                              : q.ts * exp2(((double)q.tm - TM) * P.c2d);
+      S += scaled(parts[r].m, parts[r].s, M2);
+      second += scaled(parts[r].m2nd, parts[r].s2nd, N2);
+      TS += parts[r].p_sum;
     }
-    const double total = kTail ? S + Top : S;
-    const double R = kTail && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
-    const bool has_p = TS > 0.0;
-    const double C = kTail ? TS + R : (has_p ? 1.0 : 0.0);
-    const bool has_rest = R > 0.0 && S > 0.0;
-    const double lse2 = (double)M2 + log2(total);  // log2 sum exp(z / T)
-    const double lp2 = kTail ? lse2_t : (double)TM * P.c2d + log2(TS);
-    const double scale = (double)w / (double)P.temp;
+    total = kTail ? S + second : S;
+    TS = kTail ? TS : second;
+    R = kTail && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
+    const double C = kTail ? TS + R : (TS > 0.0 ? 1.0 : 0.0);
+    if (!(S > 0.0)) R = 0.0;  // nothing outside the list: no rest class
+    const float scale_t = w * P.inv_temp / (float)total;
     RowNumbers n;
     n.m2 = M2;
-    n.f_rest = (float)(scale * (C - (has_rest ? R * total / S : 0.0)) / total);
-    n.f_top = (float)(scale * C / total);
-    n.p_sub = lp2;
-    n.q_sub = lse2;
-    n.has_p = has_p;
-    n.tail = has_rest ? R * (log(R) - log(S / total)) : 0.0;
+    n.f_rest = scale_t * (float)(R > 0.0 ? C - R * total / S : C);
+    n.f_top = scale_t * (float)C;
+    n.inv_ts = !kTail && TS > 0.0 ? 1.f / (float)TS : 0.f;
+    n.tm2 = N2;
     row_n = n;
   }
   __syncthreads();
@@ -484,130 +527,135 @@ __global__ void __launch_bounds__(kThreads, 2) k_distill(const DistillParams P) 
     return;
   }
 
-  // the gradient of entries that are not listed, in place; the listed ones
-  // read their logits first
-  const float scale = w * P.inv_temp;
-  float part = 0.f;
-  float keep_g[kKeep];
-  auto entry_loss = [&](float t, float z) -> float {  // returns the entry's gradient
-    const double lp = log2p(t, P.c2d, n.p_sub);
-    const float p = !n.has_p ? 0.f : ex2((float)lp);
-    if (p != 0.f) part = fmaf(p, (float)(lp - ((double)z * (double)P.c2 - n.q_sub)), part);
-    return n.f_top * ex2(fmaf(z, P.c2, -n.m2)) - scale * p;
-  };
-#pragma unroll
-  for (int r = 0; r < kKeep; ++r)
-    if (keep_e[r] >= 0) keep_g[r] = entry_loss(keep_t[r], Log<T>::get(zs + keep_e[r]));
-  if (grow) {
-    __syncthreads();
+  // second pass: the gradient of entries that are not listed
+  if (gs) {
     const float2 fr = make_float2(n.f_rest, n.f_rest), nn = make_float2(-n.m2, -n.m2);
-    for (int v = v_lo + tid; v < v_hi; v += kThreads) {
+    uint4* out = reinterpret_cast<uint4*>(gs) + sl.v_lo + tid;
+    auto grad = [&](const uint4& x) {
       float f[kE];
-      Log<T>::unpack(vec[v], f);
+      Log<T>::unpack(x, f);
 #pragma unroll
       for (int i = 0; i < kE; i += 2) {
-        const float2 x = ffma2(make_float2(f[i], f[i + 1]), c2v, nn);
-        const float2 g = fmul2(make_float2(ex2(x.x), ex2(x.y)), fr);
-        f[i] = g.x;
-        f[i + 1] = g.y;
+        float2 y = ffma2(make_float2(f[i], f[i + 1]), c2v, nn);
+        y = fmul2(make_float2(ex2(y.x), ex2(y.y)), fr);
+        f[i] = y.x;
+        f[i + 1] = y.y;
       }
-      vec[v] = Log<T>::pack(f);
-    }
-    if (tid < n_edge) {
-      T* p = zs + edge_at(tid);
-      Log<T>::put(p, n.f_rest * ex2(fmaf(Log<T>::get(p), P.c2, -n.m2)));
-    }
-    __syncthreads();
+      return Log<T>::pack(f);
+    };
+
+    for (int b = 0; b < n_batch; ++b) {
+      uint4 y[kUnroll];
+      if (b + 1 < n_batch) batch(y, b + 1);
+      uint4* o = out + b * (kUnroll * kThreads);
+      if (b < n_full) {
 #pragma unroll
-    for (int r = 0; r < kKeep; ++r)
-      if (keep_e[r] >= 0) Log<T>::put(zs + keep_e[r], keep_g[r]);
+        for (int u = 0; u < kUnroll; ++u) __stcs(o + u * kThreads, grad(x[u]));
+      } else {
+        const int left = n_vec - tid - b * (kUnroll * kThreads);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (u * kThreads < left) __stcs(o + u * kThreads, grad(x[u]));
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) x[u] = y[u];
+    }
+    if (tid < sl.n_edge)
+      Log<T>::put(gs + sl.edge(tid), n.f_rest * ex2(fmaf(z_edge, P.c2, -n.m2)));
+    __syncthreads();
   }
-  // entries beyond those kept: their logits are read again (nothing of the
-  // row has been written yet)
-  for (int i = tid + kKeep * kThreads; i < P.k; i += kThreads) {
-    bool ok;
-    const int e = slice_pos(i, ok);
-    if (e < 0 || (dup && !first_of(i))) continue;
-    const float g = entry_loss(teacher_at(P, list + i), Log<T>::get(zrow + c0 + e));
-    if (grow) Log<T>::put(zs + e, g);
-  }
+  // The listed entries: their gradients over it, and the loss up to the
+  // logarithms of the sums: sum p (log2 p - log2 q) = sum p (a - b) + sum p lg,
+  // a and b the exponents of p and q relative to their references, in float64
+  // (the logits may be far larger than the difference).
+  const float scale = w * P.inv_temp;
+  float part = 0.f, mass = 0.f;
+  for_entries([&](int e, float t, float z) {
+    // without a rest class the teacher's exponents, as the student's, use the
+    // rounded c2: both sides of their log-partitions then agree
+    const double a = kTail ? log2p(t, P.c2d, lse2_t) : (double)t * (double)P.c2 - (double)n.tm2;
+    const float p = kTail ? ex2((float)a) : n.inv_ts > 0.f ? ex2((float)a) * n.inv_ts : 0.f;
+    if (p != 0.f) {
+      part = fmaf(p, (float)(a - ((double)z * (double)P.c2 - (double)n.m2)), part);
+      mass += p;
+    }
+    if (gs) Log<T>::put(gs + e, n.f_top * ex2(fmaf(z, P.c2, -n.m2)) - scale * p);
+  });
   {
-    const double pd = warp_sum((double)part);
-    if (lane == 0) sm_d[0][warp] = pd;
+    const float pf = warp_sum(part), mf = warp_sum(mass);
+    if (lane == 0) sm_d[0][warp] = pf, sm_d[1][warp] = mf;
   }
-  if (grow) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncthreads();
-  if (tid == 0) {
-    if (grow && copy_bytes) {
-      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(
-                       grow + c0 + (int64_t)v_lo * kE),
-                   "r"(smem_u32(zs + v_lo * kE)), "r"(copy_bytes)
-                   : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  if (warp == 0) {
+    const double l = warp_sum(lane < kWarps ? sm_d[0][lane] : 0.0);
+    const double mass_d = warp_sum(lane < kWarps ? sm_d[1][lane] : 0.0);
+    if (lane == 0) {
+      // log2 q is b - log2 S; log2 p is a, less log2 of the listed exponentials'
+      // sum where they are normalised here
+      const double sum = mass_d > 0.0 ? l + mass_d * log2(kTail ? total : total / TS) : l;
+      if (n_parts > 1)
+        *cluster.map_shared_rank(&loss_parts[rank], 0) = sum;
+      else
+        loss_parts[0] = sum;
     }
-    double l = 0.0;
-    for (int i = 0; i < kWarps; ++i) l += sm_d[0][i];
-    if (n_parts > 1)
-      *cluster.map_shared_rank(&loss_parts[rank], 0) = l;
-    else
-      loss_parts[0] = l;
   }
-  if (grow && tid < n_edge) grow[c0 + edge_at(tid)] = zs[edge_at(tid)];
   if (n_parts > 1) cluster.sync();  // the loss parts have arrived; no CTA leaves before
-  if (tid == 0) {
-    if (rank == 0) {
-      double l = 0.0;
-      for (int r = 0; r < n_parts; ++r) l += loss_parts[r];
-      P.loss[row] = (float)((double)w * (l * 0.6931471805599453 + n.tail));
-    }
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (tid == 0 && rank == 0) {
+    double l = 0.0;
+    for (int r = 0; r < n_parts; ++r) l += loss_parts[r];
+    l *= 0.6931471805599453;
+    if (kTail && R > 0.0) l += R * (log(R) - log(S / total));
+    P.loss[row] = (float)((double)w * l);
   }
 }
 
-template <typename T, bool kTail>
-cudaError_t run(const DistillParams& P, int64_t M, int parts, cudaStream_t s) {
-  auto* k = k_distill<T, kTail>;
-  const size_t smem = (size_t)P.slice * sizeof(T) + P.slice / 8;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename T, bool kTail, int kThreads>
+cudaError_t run(const DistillParams& P, int parts, cudaStream_t s) {
+  auto* k = k_distill<T, kTail, kThreads>;
+  const size_t smem = P.slice / 8 + (size_t)P.k * 12;
+  static std::atomic<uint64_t> smem_set{0};  // one bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !((smem_set.load() >> dev) & 1u)) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) smem_set.fetch_or(1ull << dev);
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(M * parts));
+  cfg.gridDim = dim3((unsigned)(P.M * parts));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)parts;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = parts > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, P);
 }
 
 template <typename T>
-cudaError_t run_tail(const DistillParams& P, int64_t M, int parts, cudaStream_t s) {
-  return P.t_lse ? run<T, true>(P, M, parts, s) : run<T, false>(P, M, parts, s);
+cudaError_t run_tail(const DistillParams& P, int parts, cudaStream_t s) {
+  // Threads by the length of a slice: a short row is all latency, and small CTAs
+  // put more rows on an SM at once.
+  const bool small = P.slice * sizeof(T) <= kSmallSlice;
+  if (P.t_lse)
+    return small ? run<T, true, 128>(P, parts, s) : run<T, true, kBigThreads>(P, parts, s);
+  return small ? run<T, false, 128>(P, parts, s) : run<T, false, kBigThreads>(P, parts, s);
 }
 
 }  // namespace
 
-int take_distill_status() {
-  int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_distill_status, sizeof(int)) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_distill_status, &zero, sizeof(int));
-  return v;
-}
-
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
   const int64_t esz = a.dtype == LQ_F32 ? 4 : 2;
-  // CTAs per row: as few as let two of them share an SM (their copies and
-  // passes then overlap), more while the SMs are not all busy and a slice
-  // still is worth its own CTA
+  // CTAs per row: one, unless the rows are too few to keep the SMs busy and a
+  // slice is still worth its own CTA
   int parts = 1;
   auto slice_of = [&](int n) { return ((a.V + 8 + n - 1) / n + 31) / 32 * 32; };
-  while (parts < kMaxCluster && slice_of(parts) * esz > 100 * 1024) parts *= 2;
   while (parts < kMaxCluster && a.M * parts < 2 * num_sms() && slice_of(parts) * esz > 8 * 1024)
     parts *= 2;
   DistillParams P{};
@@ -618,6 +666,7 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
   P.t_lse = a.t_lse;
   P.weight = a.weight;
   P.loss = a.loss;
+  P.M = a.M;
   P.V = a.V;
   P.k = a.k;
   P.t_dtype = a.t_dtype;
@@ -627,9 +676,9 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
   P.inv_temp = 1.f / a.temp;
   P.c2d = 1.4426950408889634 / (double)a.temp;
   P.c2 = (float)P.c2d;
-  if (a.dtype == LQ_F32) return run_tail<float>(P, a.M, parts, s);
-  if (a.dtype == LQ_BF16) return run_tail<__nv_bfloat16>(P, a.M, parts, s);
-  return run_tail<__half>(P, a.M, parts, s);
+  if (a.dtype == LQ_F32) return run_tail<float>(P, parts, s);
+  if (a.dtype == LQ_BF16) return run_tail<__nv_bfloat16>(P, parts, s);
+  return run_tail<__half>(P, parts, s);
 }
 
 }  // namespace lq

@@ -742,23 +742,19 @@ lq_status read_and_clear_device_status(cudaStream_t s) {
     if (e != cudaSuccess) return cuda_error(e, "clear device status");
     take_chain_status();  // one report covers all status words
     take_dense_status();
-    take_distill_status();
     set_error("a bounded device-side wait expired in the GEMM kernel (status %d)", v);
     return (lq_status)v;
   }
   v = take_chain_status();
   if (v != 0) {
     take_dense_status();
-    take_distill_status();
     set_error("a grid barrier of the persistent decode kernel gave up (status %d)", v);
     return (lq_status)v;
   }
   v = take_dense_status();
-  const int v2 = take_distill_status();
-  if (v != 0 || v2 != 0) {
-    set_error("a bounded device-side wait expired in a %s kernel (status %d)",
-              v != 0 ? "dense" : "distillation", v != 0 ? v : v2);
-    return (lq_status)(v != 0 ? v : v2);
+  if (v != 0) {
+    set_error("a bounded device-side wait expired in a dense kernel (status %d)", v);
+    return (lq_status)v;
   }
   return LQ_OK;
 }

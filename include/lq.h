@@ -444,11 +444,12 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *               logits hold.
  *   d_loss      out M float32;  d_grad  out M x V of dtype, or NULL; it may be
  *               d_logits itself (in place), no other overlap.
- * 1 <= k <= V; a row's logits are at most LQ_DISTILL_MAX_ROW_BYTES
- * (LQ_ERR_SHAPE); temp > 0.  Sums are float32 over up to a few hundred values
- * of a thread, float64 beyond.  Asynchronous on `stream`; safe to capture.
+ * 1 <= k <= min(V, LQ_DISTILL_MAX_K) and V <= LQ_DISTILL_MAX_V (LQ_ERR_SHAPE);
+ * temp > 0.  A thread and a warp sum in float32, a row in float64.  Asynchronous
+ * on `stream`; safe to capture; two runs of a call give the same bits.
  */
-#define LQ_DISTILL_MAX_ROW_BYTES (8ll * 192 * 1024)
+#define LQ_DISTILL_MAX_K 8192
+#define LQ_DISTILL_MAX_V (512 * 1024)
 lq_status lq_distill_loss(const void* d_logits, int32_t dtype, int64_t M, int64_t V,
                           const void* d_t_values, int32_t t_dtype, const void* d_t_index,
                           int32_t idx_bytes, int64_t k, const float* d_t_lse,

@@ -118,9 +118,7 @@ def test_distill_refusals(L):
                dict(temp=float("nan")), dict(temp=float("inf")), dict(temp=1e-45), dict(z=None),
                dict(t=None), dict(i=None), dict(loss=None)):
         assert distill(L, **kw) == lq.LQ_ERR_ARG, kw
-    most = 8 * 192 * 1024
-    for kw in (dict(k=101), dict(V=most // 2 + 1), dict(V=most // 4 + 1, dt=lq.LQ_F32),
-               dict(M=1 << 30)):
+    for kw in (dict(k=101), dict(k=8193, V=20000), dict(V=512 * 1024 + 1), dict(M=1 << 30)):
         assert distill(L, **kw) == lq.LQ_ERR_SHAPE, kw
     for kw in (dict(z=X + 2), dict(t=W + 4), dict(i=Z + 8), dict(loss=Y + 4), dict(grad=R + 2),
                dict(lse=R + 4), dict(w=R + 4)):
@@ -132,7 +130,8 @@ def test_distill_refusals(L):
 
 def test_header_limit_matches():
     text = open(B.INCLUDE + "/lq.h").read()
-    assert "#define LQ_DISTILL_MAX_ROW_BYTES (8ll * 192 * 1024)" in text
+    assert "#define LQ_DISTILL_MAX_V (512 * 1024)" in text
+    assert "#define LQ_DISTILL_MAX_K 8192" in text
     for name, code in (("NONE", 0), ("RELU", 1), ("SILU", 2), ("GELU", 3), ("GELU_TANH", 4)):
         assert getattr(lq, "LQ_ACT_" + name) == code == lq.LQ_ACTS[name.lower()]
         assert any(line.split()[:3] == ["#define", "LQ_ACT_" + name, str(code)]

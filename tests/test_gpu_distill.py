@@ -148,7 +148,7 @@ def test_wide_rows_over_every_cluster_size():
     """One row and many, so that a row is one slice, two, four or eight."""
     for M, V, dt in ((1, 1000, "bf16"), (40, 20011, "bf16"), (90, 20011, "f32"),
                      (160, 20011, "f16"), (300, 20011, "bf16"), (2, 380001, "f32"),
-                     (1, 786425, "bf16")):
+                     (1, 524288, "bf16")):
         teacher, z, tv, ti = case(V, M, V, 50, TYPES[dt])
         rows = slice(0, min(M, 6))
         L, G, tl, tg = oracle(z[rows], tv[rows], ti[rows], None, None, 1.0)
