@@ -34,7 +34,6 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
-#include <type_traits>
 
 #include "lq_dense.cuh"
 
@@ -390,6 +389,34 @@ struct Cfg {
   static constexpr int kTmemCols = 2 * kBN;
 };
 
+// Eight 16-bit elements at any element offset of a 16-byte aligned array of
+// `total`: the two aligned vectors around them, shifted together.  Near the end
+// of the array one by one (zero beyond it).
+__device__ __forceinline__ uint4 load8_any(const uint16_t* base, int64_t at, int64_t total) {
+  const int m = (int)(at & 7);
+  const int64_t a0 = at - m;
+  if (a0 + 16 > total) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at + e < total) w[e / 2] |= (uint32_t)base[at + e] << (16 * (e % 2));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  const uint4* p = reinterpret_cast<const uint4*>(base + a0);
+  const uint4 x = p[0], y = p[1];
+  // a shift by m elements in three steps of 4, 2 and 1
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t u[6], v[5];
+#pragma unroll
+  for (int i = 0; i < 6; ++i) u[i] = (m & 4) ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) v[i] = (m & 2) ? u[i + 1] : u[i];
+  if (m & 1)
+    return make_uint4(__funnelshift_r(v[0], v[1], 16), __funnelshift_r(v[1], v[2], 16),
+                      __funnelshift_r(v[2], v[3], 16), __funnelshift_r(v[3], v[4], 16));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // 32 x kUnit values of one warp in shared memory: row = lane, 16-byte pieces
 // XOR-swizzled so that both the row-per-lane accesses and the row-piece-per-
 // lane accesses are free of bank conflicts
@@ -430,83 +457,69 @@ __device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, c
     }
     return;
   }
-  constexpr int kElems = kRowBytes / kEsz;
+  if (kEsz != 2) return;  // float32 rows are whole pieces
+  // Rows that start anywhere: lane l holds the word of elements 2l and 2l + 1.
+  // Where the row starts inside a 4-byte word the words are shifted by one
+  // element, and the first and the last element go alone.
+  constexpr int kWords = kRowBytes / 4;
+  const int64_t left = N - col0;  // columns of this unit that exist
+  const int n = left < 2 * kWords ? (int)left : 2 * kWords;
+#pragma unroll 8
   for (int row = 0; row < 32; ++row) {
+    uint32_t w = 0;
+    if (lane < kWords)
+      w = *reinterpret_cast<const uint32_t*>(stg + piece_at<kRowBytes>(row, lane / 4) +
+                                             (lane % 4) * 4);
+    const uint32_t next = __shfl_down_sync(~0u, w, 1);
     char* dst = map(row0 + row);
     if (!dst) continue;
-#pragma unroll
-    for (int e = 0; e < kElems; e += 32) {
-      const int i = e + lane;
-      const int64_t c = col0 + i;
-      if (c >= N) continue;
-      const unsigned char* src =
-          stg + piece_at<kRowBytes>(row, i / kPer) + (i % kPer) * kEsz;
-      if (kEsz == 2)
-        *reinterpret_cast<uint16_t*>(dst + c * 2) = *reinterpret_cast<const uint16_t*>(src);
-      else
-        *reinterpret_cast<uint32_t*>(dst + c * 4) = *reinterpret_cast<const uint32_t*>(src);
-    }
+    uint16_t* d = reinterpret_cast<uint16_t*>(dst) + col0;
+    const int odd = ((uintptr_t)d & 2) ? 1 : 0;
+    const int e = 2 * lane + odd;  // first element of this lane's word
+    if (odd) w = __funnelshift_r(w, next, 16);
+    if (e + 1 < n) *reinterpret_cast<uint32_t*>(d + e) = w;
+    // what no whole word covers: the first element, and the last where one is left
+    const int tail = (n - odd) & 1;
+    if (lane == 0 && odd)
+      d[0] = *reinterpret_cast<const uint16_t*>(stg + piece_at<kRowBytes>(row, 0));
+    if (lane == 1 && tail)
+      d[n - 1] = *reinterpret_cast<const uint16_t*>(
+          stg + piece_at<kRowBytes>(row, (n - 1) / 8) + ((n - 1) % 8) * 2);
   }
 }
 
-// global rows -> shared-memory unit (16-bit elements); what lies outside the
-// matrix is left as it is
+// A unit of 16-bit elements of global rows, in two steps: the loads, which may
+// travel while something else is done, and their pieces put into shared memory.
+// What lies outside the matrix is zero.
 template <int kRowBytes>
-__device__ __forceinline__ void fill_unit(unsigned char* stg, int lane, const uint16_t* src,
-                                          int64_t ld, int64_t row0, int64_t col0, int64_t M,
-                                          int64_t N, bool vec) {
-  constexpr int kPieces = kRowBytes / 16;
-  if (vec) {
-    uint4 v[kPieces];
+struct UnitLoad {
+  static constexpr int kPieces = kRowBytes / 16;
+  uint4 v[kPieces];
+  __device__ __forceinline__ void load(int lane, const uint16_t* src, int64_t ld, int64_t row0,
+                                       int64_t col0, int64_t M, int64_t N, bool vec) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
-      const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
-      const int64_t r = row0 + row, c = col0 + pc * 8;
+      const int64_t r = row0 + j * (32 / kPieces) + lane / kPieces;
+      const int64_t c = col0 + (lane % kPieces) * 8;
       v[j] = make_uint4(0, 0, 0, 0);
-      if (r < M && c < N) v[j] = *reinterpret_cast<const uint4*>(src + r * ld + c);
-    }
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-      const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
-      *reinterpret_cast<uint4*>(stg + piece_at<kRowBytes>(row, pc)) = v[j];
-    }
-    return;
-  }
-  for (int row = 0; row < 32; ++row) {
-    const int64_t r = row0 + row;
-    if (r >= M) continue;
-#pragma unroll
-    for (int e = 0; e < kRowBytes / 2; e += 32) {
-      const int i = e + lane;
-      const int64_t c = col0 + i;
-      if (c < N)
-        *reinterpret_cast<uint16_t*>(stg + piece_at<kRowBytes>(row, i / 8) + (i % 8) * 2) =
-            src[r * ld + c];
+      if (r >= M || c >= N) continue;
+      // (elements past the row's end are the next row's: they are not stored)
+      v[j] = vec ? *reinterpret_cast<const uint4*>(src + r * ld + c)
+                 : load8_any(src, r * ld + c, M * ld);
     }
   }
-}
+  __device__ __forceinline__ void put(unsigned char* stg, int lane) const {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j)
+      *reinterpret_cast<uint4*>(stg + piece_at<kRowBytes>(j * (32 / kPieces) + lane / kPieces,
+                                                          lane % kPieces)) = v[j];
+  }
+};
 
-// v[i] += bias[col + i] (columns past N: unchanged)
-template <typename T>
-__device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t* bias, int64_t col,
-                                         int64_t N) {
-  if (col + 32 <= N) {
+// v[i] += the bias that lane i holds
+__device__ __forceinline__ void add_bias(float (&v)[32], float own) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(bias + col + i));
-      const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Elem<T>::unpack(q[e]);
-        v[i + 2 * e] += f.x;
-        v[i + 2 * e + 1] += f.y;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (col + i < N) v[i] += Elem<T>::load(bias + col + i);
-  }
+  for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(~0u, own, i);
 }
 
 template <typename T, int kRowBytes>
@@ -603,30 +616,29 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
   pdl_wait();  // everything below reads or writes global memory
 
   if (warp == C::kEpiWarps) {
-    // ---- TMA producer
-    const bool leader = elect_one();
-    int it = 0, st = 0;
-    uint32_t ph = 1u;  // parity to wait for: the ring starts out empty
-    bool ok = true;
-    for (int t = t_first; t < n_tiles && ok; t += t_step) {
-      int im, in;
-      tile_at(t, tm, tn, im, in);
-      const int m0 = im * kTileM + rank * BM;
-      const int n0 = in * kTileN + (kEpi == kEpiGated ? 0 : rank * (kBN / kPair));
-      for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
-        if (!wait_bounded(bar_empty + 8 * st, ph, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const bool first = kb < P.n_kb1;
-        const CUtensorMap* a = first ? &tmA : &tmA2;
-        const CUtensorMap* b = first ? &tmB : &tmB2;
-        const int k0 = (first ? kb : kb - P.n_kb1) * BK;
-        // a stage is full once the bytes of both CTAs have arrived at the
-        // first one's barrier, where the MMAs are issued
-        const uint32_t full = kPair == 1 ? bar_full + 8 * st : in_first_cta(bar_full + 8 * st);
-        const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
-        if (leader) {
+    // ---- TMA producer: one lane runs the whole loop
+    if (elect_one()) {
+      int it = 0, st = 0;
+      uint32_t ph = 1u;  // parity to wait for: the ring starts out empty
+      bool ok = true;
+      for (int t = t_first; t < n_tiles && ok; t += t_step) {
+        int im, in;
+        tile_at(t, tm, tn, im, in);
+        const int m0 = im * kTileM + rank * BM;
+        const int n0 = in * kTileN + (kEpi == kEpiGated ? 0 : rank * (kBN / kPair));
+        for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
+          if (!wait_bounded(bar_empty + 8 * st, ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const bool first = kb < P.n_kb1;
+          const CUtensorMap* a = first ? &tmA : &tmA2;
+          const CUtensorMap* b = first ? &tmB : &tmB2;
+          const int k0 = (first ? kb : kb - P.n_kb1) * BK;
+          // a stage is full once the bytes of both CTAs have arrived at the
+          // first one's barrier, where the MMAs are issued
+          const uint32_t full = kPair == 1 ? bar_full + 8 * st : in_first_cta(bar_full + 8 * st);
+          const uint32_t sa = base + st * C::kStageA, sb = base + C::kOffB + st * C::kStageB;
           if (rank == 0) mbar_arrive_expect_tx(bar_full + 8 * st, C::kStageBytes * kPair);
           if (kAMn) {
 #pragma unroll
@@ -648,22 +660,21 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
           } else {
             load_tile<kPair>(sb, b, full, k0, n0);
           }
+          if (++st == C::kStages) st = 0, ph ^= 1u;
         }
-        __syncwarp();
-        if (++st == C::kStages) st = 0, ph ^= 1u;
       }
+      // no copy is in flight when the CTA leaves
+      if (rank == 0)
+        for (int i = max(0, it - C::kStages); i < it; ++i)
+          wait_drain(bar_full + 8 * (i % C::kStages), (uint32_t)(i / C::kStages) & 1u);
     }
-    if (rank == 0)
-      for (int i = max(0, it - C::kStages); i < it; ++i)
-        wait_drain(bar_full + 8 * (i % C::kStages), (uint32_t)(i / C::kStages) & 1u);
   } else if (warp == C::kEpiWarps + 1) {
-    // ---- MMA issuer (of a pair: the first CTA's, for both)
-    if (rank == 0) {
+    // ---- MMA issuer (of a pair: the first CTA's, for both): one lane
+    if (rank == 0 && elect_one()) {
       constexpr uint32_t idesc = instr_desc(Elem<T>::kFormat, kAMn, kBMn, kTileM, kBN);
       // descriptor units (16 bytes) between consecutive 16-wide contraction steps
       constexpr uint64_t stepA = (kAMn ? 2048u : 32u) >> 4, stepB = (kBMn ? 2048u : 32u) >> 4;
       const uint64_t descA = smem_desc(base, kAMn), descB = smem_desc(base + C::kOffB, kBMn);
-      const bool leader = elect_one();
       int st = 0, j = 0;
       uint32_t ph = 0u;
       bool ok = true;
@@ -678,22 +689,17 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
             break;
           }
           tc_fence_after();
-          if (leader) {
-            const uint64_t da = descA + (uint64_t)(st * (C::kStageA >> 4));
-            const uint64_t db = descB + (uint64_t)(st * (C::kStageB >> 4));
+          const uint64_t da = descA + (uint64_t)(st * (C::kStageA >> 4));
+          const uint64_t db = descB + (uint64_t)(st * (C::kStageB >> 4));
 #pragma unroll
-            for (int i = 0; i < BK / 16; ++i)
-              umma_f16<kPair>(d, da + stepA * i, db + stepB * i, idesc, (kb | i) ? 1u : 0u);
-            commit_all<kPair>(bar_empty + 8 * st);
-          }
-          __syncwarp();
+          for (int i = 0; i < BK / 16; ++i)
+            umma_f16<kPair>(d, da + stepA * i, db + stepB * i, idesc, (kb | i) ? 1u : 0u);
+          commit_all<kPair>(bar_empty + 8 * st);
           if (++st == C::kStages) st = 0, ph ^= 1u;
         }
-        if (ok && leader) commit_all<kPair>(bar_accf + 8 * buf);
-        __syncwarp();
+        if (ok) commit_all<kPair>(bar_accf + 8 * buf);
       }
-      if (leader) commit_all<kPair>(bar_drain);
-      __syncwarp();
+      commit_all<kPair>(bar_drain);
       wait_drain(bar_drain, 0u);
     }
   } else {
@@ -701,43 +707,62 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
     const int q = warp & 3, part = warp >> 2;
     unsigned char* stg = gbase + C::kOffStaging + warp * 4096;
     constexpr int kRowBytes = C::kUnit * (kEpi == kEpiF32 ? 4 : 2);
+    constexpr int kParts = C::kCols / 32;  // 32-column parts of this warp
     int j = 0;
     for (int t = t_first; t < n_tiles; t += t_step, ++j) {
       int im, in;
       tile_at(t, tm, tn, im, in);
       const int buf = j & 1;
       const int64_t row0 = (int64_t)im * kTileM + rank * BM + 32 * q;
-      const int64_t n0 = (int64_t)in * kTileN;
+      const int64_t n0 = (int64_t)in * kTileN + part * C::kCols;  // this warp's first column
       const bool live = row0 < P.M;
-      if (!wait_bounded(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag))
-        break;
+      // while the products are under way: the bias (lane l holds column l of every
+      // part) and the first unit of the residual
+      float own[kParts], own2[kParts];
+      UnitLoad<kRowBytes> res;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const int64_t c = n0 + 32 * k + lane;
+        own[k] = (kEpi == kEpiDense || kEpi == kEpiGated) && P.bias && c < P.N
+                     ? Elem<T>::load(P.bias + c) : 0.f;
+        own2[k] = kEpi == kEpiGated && P.bias2 && c < P.N ? Elem<T>::load(P.bias2 + c) : 0.f;
+      }
+      if (kEpi == kEpiDense && P.res && live)
+        res.load(lane, P.res, P.ldo, row0, n0, P.M, P.N, P.vec);
+      auto of_part = [&](const float (&o)[kParts], int k) {
+        float b = o[0];
+#pragma unroll
+        for (int i = 1; i < kParts; ++i) b = k == i ? o[i] : b;
+        return b;
+      };
+      if (!wait_bounded(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag)) break;
       tc_fence_after();
-      const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) + (uint32_t)(buf * kBN);
+      const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) +
+                           (uint32_t)(buf * kBN + part * C::kCols);
       const RowMap map = {P.M,          P.rows1,       P.split,
                           (char*)P.out, (char*)P.out2, P.ldo * (kEpi == kEpiF32 ? 4 : 2)};
       for (int u = 0; u < C::kCols; u += C::kUnit) {
-        const int tc = part * C::kCols + u;  // tile column of this unit
-        const int64_t col = n0 + tc;
+        const int64_t col = n0 + u;
         if (!live || col >= P.N) continue;
-        if (kEpi == kEpiDense && P.aux) {
-          for (int c = 0; c < C::kUnit; c += 32) {
-            float v[32];
-            load_acc(acc + tc + c, v);
-            if (P.bias) add_bias<T>(v, P.bias, col + c, P.N);
-            put_row<T, kRowBytes>(stg, lane, c, v);
-          }
-          __syncwarp();
-          const RowMap za = {P.M, P.M, P.M, (char*)P.aux, nullptr, P.ldo * 2};
-          flush_unit<kRowBytes, 2>(stg, lane, za, row0, col, P.N, P.vec);
-          __syncwarp();
-        }
-        if (kEpi == kEpiGated && P.aux) {
-          for (int f = 0; f < 2; ++f) {
+        // accumulator columns of this warp from u + c on, with the bias
+        auto take = [&](int c, float (&v)[32]) {
+          load_acc(acc + u + c, v);
+          if ((kEpi == kEpiDense || kEpi == kEpiGated) && P.bias)
+            add_bias(v, of_part(own, (u + c) / 32));
+        };
+        auto take_up = [&](int c, float (&v)[32]) {
+          load_acc(acc + kTileN + u + c, v);
+          if (P.bias2) add_bias(v, of_part(own2, (u + c) / 32));
+        };
+        if ((kEpi == kEpiDense || kEpi == kEpiGated) && P.aux) {
+          // what the backward pass reads
+          for (int f = 0; f < (kEpi == kEpiGated ? 2 : 1); ++f) {
             for (int c = 0; c < C::kUnit; c += 32) {
               float v[32];
-              load_acc(acc + f * kTileN + tc + c, v);
-              const uint16_t* b = f ? P.bias2 : P.bias;
-              if (b) add_bias<T>(v, b, col + c, P.N);
+              if (f)
+                take_up(c, v);
+              else
+                take(c, v);
               put_row<T, kRowBytes>(stg, lane, c, v);
             }
             __syncwarp();
@@ -747,23 +772,22 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
           }
         }
         if (kEpi == kEpiDense && P.res) {
-          fill_unit<kRowBytes>(stg, lane, P.res, P.ldo, row0, col, P.M, P.N, P.vec);
+          res.put(stg, lane);
           __syncwarp();
+          if (u + C::kUnit < C::kCols)
+            res.load(lane, P.res, P.ldo, row0, col + C::kUnit, P.M, P.N, P.vec);
         }
         for (int c = 0; c < C::kUnit; c += 32) {
           float v[32];
-          load_acc(acc + tc + c, v);
+          take(c, v);
           if (kEpi == kEpiDense) {
-            if (P.bias) add_bias<T>(v, P.bias, col + c, P.N);
             apply_act(P.act, v);
             if (P.res) add_row<T, kRowBytes>(stg, lane, c, v);
           }
           if (kEpi == kEpiGated) {
-            if (P.bias) add_bias<T>(v, P.bias, col + c, P.N);
             apply_act(P.act, v);
             float w[32];
-            load_acc(acc + kTileN + tc + c, w);
-            if (P.bias2) add_bias<T>(w, P.bias2, col + c, P.N);
+            take_up(c, w);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] *= w[i];
           }
@@ -968,17 +992,13 @@ __device__ __forceinline__ void unpack_vec(const uint4& w, float (&f)[8]) {
     f[2 * e + 1] = v.y;
   }
 }
-template <typename T>
-__device__ __forceinline__ void unpack_vec(uint16_t w, float (&f)[1]) {
-  f[0] = Elem<T>::load(&w);
-}
-
-// A block covers 32 kVec columns of one row block: a thread owns kVec
-// neighbouring columns and every 8th row, keeps their float32 sums in
-// registers, and the eight row groups are added in shared memory in order.
-template <typename T, int kVec, bool kGated, int kAct>
+// A block covers 256 columns of one row block: a thread owns eight neighbouring
+// columns and every 8th row, keeps their float32 sums in registers, and the eight
+// row groups are added in shared memory in order.  kWhole: rows start on 16-byte
+// boundaries (N a multiple of 8).
+template <typename T, bool kWhole, bool kGated, int kAct>
 __global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
-  constexpr int kF = kGated ? 2 : 1;
+  constexpr int kF = kGated ? 2 : 1, kVec = 8;
   __shared__ float red[8][kF][32 * kVec];
   const int lane = threadIdx.x & 31, rg = threadIdx.x >> 5;
   const int64_t half = kGated ? P.ldz / 2 : P.ldz;
@@ -992,19 +1012,22 @@ __global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) sum[f][i] = 0.f;
   if (c0 < half) {
-    const bool in = c0 < P.N;  // kVec > 1: N is a multiple of kVec
-    constexpr int kRows = kVec == 8 ? 4 : 8;  // rows whose loads travel together
-    using Load = typename std::conditional<kVec == 8, uint4, uint16_t>::type;
+    const bool in = c0 < P.N;
+    constexpr int kRows = 4;  // rows whose loads travel together
+    const int64_t total = P.M * P.N;
     for (int64_t rb = r0 + rg; rb < r1; rb += 8 * kRows) {
-      Load la[kRows], lb[kRows], lc[kRows];
+      uint4 la[kRows], lb[kRows], lc[kRows];
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         const int64_t r = rb + 8 * j, at = r * P.N + c0;
-        la[j] = lb[j] = lc[j] = Load{};
+        la[j] = lb[j] = lc[j] = make_uint4(0, 0, 0, 0);
         if (in && r < r1) {
-          la[j] = __ldg(reinterpret_cast<const Load*>(P.dy + at));
-          if (kAct != LQ_ACT_NONE || kGated) lb[j] = __ldg(reinterpret_cast<const Load*>(P.z + at));
-          if (kGated) lc[j] = __ldg(reinterpret_cast<const Load*>(P.u + at));
+          auto load = [&](const uint16_t* p) {
+            return kWhole ? __ldg(reinterpret_cast<const uint4*>(p + at)) : load8_any(p, at, total);
+          };
+          la[j] = load(P.dy);
+          if (kAct != LQ_ACT_NONE || kGated) lb[j] = load(P.z);
+          if (kGated) lc[j] = load(P.u);
         }
       }
 #pragma unroll
@@ -1022,7 +1045,7 @@ __global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
           o[0][i] = kGated ? dy[i] * u[i] * da : dy[i] * da;
           if (kGated) o[kF - 1][i] = dy[i] * a;
           // columns past N are padding of the contraction: exactly zero
-          if (!in) o[0][i] = o[kF - 1][i] = 0.f;
+          if (kWhole ? !in : c0 + i >= P.N) o[0][i] = o[kF - 1][i] = 0.f;
         }
 #pragma unroll
         for (int f = 0; f < kF; ++f) {
@@ -1030,16 +1053,12 @@ __global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
           for (int i = 0; i < kVec; ++i) sum[f][i] += o[f][i];
           if (P.dz) {
             uint16_t* dst = P.dz + r * P.ldz + f * half + c0;
-            if (kVec == 8) {
-              uint4 w;
-              w.x = Elem<T>::pack(o[f][0], o[f][1 % kVec]);
-              w.y = Elem<T>::pack(o[f][2 % kVec], o[f][3 % kVec]);
-              w.z = Elem<T>::pack(o[f][4 % kVec], o[f][5 % kVec]);
-              w.w = Elem<T>::pack(o[f][6 % kVec], o[f][7 % kVec]);
-              *reinterpret_cast<uint4*>(dst) = w;
-            } else {
-              *dst = Elem<T>::round(o[f][0]);
-            }
+            uint4 w;
+            w.x = Elem<T>::pack(o[f][0], o[f][1]);
+            w.y = Elem<T>::pack(o[f][2], o[f][3]);
+            w.z = Elem<T>::pack(o[f][4], o[f][5]);
+            w.w = Elem<T>::pack(o[f][6], o[f][7]);
+            *reinterpret_cast<uint4*>(dst) = w;
           }
         }
       }
@@ -1171,12 +1190,12 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
 
 // Tile shape, by the time it would take.  Clocks of one 64-wide contraction
 // block: 512 for the 256 x 256 tile of a CTA pair (the tensor pipe's own time),
-// 330 for its 256 x 128 tile, 366 for a CTA's own 128 x 128 and 350 for its
-// 128 x 64 tile (what issuing the copies and MMAs takes); a tile's last
-// epilogue and a pair's handshakes come on top once.  Measured on
-// 2048 x 2048 x 5632: 35.6, 37.8, 43.1 and 71.7 us; on 16384 x 5632 x 2048:
-// 250, 320, 419 and 625; on 256 x 2048 x 2048: 15.7, 10.0, 10.4 and 9.9; on
-// 2048 x 256 x 256: 8.5, 5.3, 4.9 and 4.5.
+// 300 for its 256 x 128 tile, 330 for a CTA's own 128 x 128 and 285 for its
+// 128 x 64 tile (what the operand tiles take from L2); a tile's last epilogue and
+// a pair's handshakes come on top once.  Measured on 2048 x 2048 x 5632: 34.2,
+// 34.7, 38.9 and 56.2 us; on 16384 x 5632 x 2048: 251, 281, 331 and 466; on
+// 128 x 2048 x 2048: 14.2, 9.1, 8.9 and 8.2; on 2048 x 256 x 256: 6.4, 5.0, 4.5
+// and 4.2.
 template <typename T, bool kAMn, bool kBMn, int kEpi>
 cudaError_t pick_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
                       const GemmParams& P, cudaStream_t s) {
@@ -1186,8 +1205,9 @@ cudaError_t pick_gemm(const Operand& a, const Operand& a2, const Operand& b, con
     return (tiles + slots - 1) / slots * P.n_kb * per_block + once;
   };
   const int sms = num_sms();
-  const int64_t c2256 = clocks(256, 256, sms / 2, 512, 7800), c2128 = clocks(256, 128, sms / 2, 330, 4300),
-                c128 = clocks(128, 128, sms, 366, 3000), c64 = clocks(128, 64, sms, 350, 2600);
+  const int64_t c2256 = clocks(256, 256, sms / 2, 512, 7800),
+                c2128 = clocks(256, 128, sms / 2, 300, 4300),
+                c128 = clocks(128, 128, sms, 330, 3000), c64 = clocks(128, 64, sms, 285, 2600);
   const int64_t best = std::min(std::min(c2256, c2128), std::min(c128, c64));
   if (best == c2256) return run_gemm<T, 256, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
   if (best == c2128) return run_gemm<T, 128, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
@@ -1243,20 +1263,20 @@ cudaError_t forward(const DenseForward& d, cudaStream_t s) {
   return pick_gemm<T, false, false, kEpiDense>(x, x, w, w, P, s);
 }
 
-template <typename T, int kVec, bool kGated>
+template <typename T, bool kWhole, bool kGated>
 cudaError_t act_grad_launch(const GradParams& P, dim3 grid, cudaStream_t s) {
   switch (P.act) {
     case LQ_ACT_RELU:
-      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_RELU>, grid, dim3(256), 0, s, true, P);
+      return launch_kernel(k_act_grad<T, kWhole, kGated, LQ_ACT_RELU>, grid, dim3(256), 0, s, true, P);
     case LQ_ACT_SILU:
-      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_SILU>, grid, dim3(256), 0, s, true, P);
+      return launch_kernel(k_act_grad<T, kWhole, kGated, LQ_ACT_SILU>, grid, dim3(256), 0, s, true, P);
     case LQ_ACT_GELU:
-      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_GELU>, grid, dim3(256), 0, s, true, P);
+      return launch_kernel(k_act_grad<T, kWhole, kGated, LQ_ACT_GELU>, grid, dim3(256), 0, s, true, P);
     case LQ_ACT_GELU_TANH:
-      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_GELU_TANH>, grid, dim3(256), 0, s,
+      return launch_kernel(k_act_grad<T, kWhole, kGated, LQ_ACT_GELU_TANH>, grid, dim3(256), 0, s,
                            true, P);
     default:
-      return launch_kernel(k_act_grad<T, kVec, kGated, LQ_ACT_NONE>, grid, dim3(256), 0, s, true, P);
+      return launch_kernel(k_act_grad<T, kWhole, kGated, LQ_ACT_NONE>, grid, dim3(256), 0, s, true, P);
   }
 }
 
@@ -1282,13 +1302,15 @@ cudaError_t backward(const DenseBackward& d, cudaStream_t s) {
     G.ldz = pl.ldz;
     G.rows = pl.rows;
     G.act = d.act;
-    const bool vec = d.N % 8 == 0;
-    const int64_t width = gated ? pl.ldz / 2 : pl.ldz, per = vec ? 256 : 32;
-    const dim3 grid((unsigned)((width + per - 1) / per), (unsigned)pl.row_blocks);
+    const bool whole = d.N % 8 == 0;
+    const int64_t width = gated ? pl.ldz / 2 : pl.ldz;
+    const dim3 grid((unsigned)((width + 255) / 256), (unsigned)pl.row_blocks);
     if (gated)
-      e = vec ? act_grad_launch<T, 8, true>(G, grid, s) : act_grad_launch<T, 1, true>(G, grid, s);
+      e = whole ? act_grad_launch<T, true, true>(G, grid, s)
+                : act_grad_launch<T, false, true>(G, grid, s);
     else
-      e = vec ? act_grad_launch<T, 8, false>(G, grid, s) : act_grad_launch<T, 1, false>(G, grid, s);
+      e = whole ? act_grad_launch<T, true, false>(G, grid, s)
+                : act_grad_launch<T, false, false>(G, grid, s);
     if (e != cudaSuccess) return e;
   }
   if (sums) {

@@ -227,11 +227,12 @@ def test_many_tiles_and_long_contractions():
     check_gated_bwd(9000, 1000, 512, torch.bfloat16, lq.LQ_ACT_SILU)
 
 
-def test_residual_in_place_and_repeatable():
+@pytest.mark.parametrize("N", [200, 201, 130, 195])
+def test_residual_in_place_and_repeatable(N):
     dt = torch.bfloat16
     for M in (6, 333):
-        x, w = normal(1, M, 128, dtype=dt), normal(2, 200, 128, dtype=dt)
-        r = normal(3, M, 200, dtype=dt)
+        x, w = normal(1, M, 128, dtype=dt), normal(2, N, 128, dtype=dt)
+        r = normal(3, M, N, dtype=dt)
         want, _ = lq.lq_dense_linear(x, w, residual=r)
         again, _ = lq.lq_dense_linear(x, w, residual=r)
         assert torch.equal(want, again)
@@ -242,7 +243,8 @@ def test_residual_in_place_and_repeatable():
 def test_rows_behind_the_output_stay():
     """Neither the rows behind the last one nor the values after an odd row end
     are written."""
-    for M, N, K in ((5, 9, 16), (100, 9, 16), (129, 65, 64), (300, 200, 64)):
+    for M, N, K in ((5, 9, 16), (100, 9, 16), (129, 65, 64), (300, 200, 64), (131, 130, 64),
+                    (333, 703, 64)):
         buf = torch.full((M * N + 4096,), 7.0, dtype=torch.float16, device="cuda")
         y = buf[:M * N].view(M, N)
         lq.lq_dense_linear(normal(1, M, K, dtype=torch.float16),
