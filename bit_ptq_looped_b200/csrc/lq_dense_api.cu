@@ -126,27 +126,19 @@ lq_status launched(cudaError_t e, const char* what) {
 
 extern "C" {
 
-int64_t lq_dense_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return bad_extent(M, N, K) ? -1 : 0;
-}
-
 lq_status lq_dense_linear(const void* d_x, const void* d_w, const void* d_bias,
                           const void* d_residual, int32_t dtype, int64_t M, int64_t N, int64_t K,
-                          int32_t act, void* d_y, void* d_z, void* d_ws, int64_t ws_bytes,
-                          void* stream) {
+                          int32_t act, void* d_y, void* d_z, void* stream) {
   lq_status st = check_dense(dtype, M, N, K, act);
   if (st != LQ_OK || M == 0) return st;
   if (!d_x || !d_w || !d_y) return null_pointer("x, W or y");
-  const int64_t need = lq_dense_linear_workspace_bytes(M, N, K);
   const Buf bufs[] = {{"x", d_x, M * K * 2, false},
                       {"W", d_w, N * K * 2, false},
                       {"the bias", d_bias, N * 2, false},
                       {"the residual", d_residual == d_y ? nullptr : d_residual, M * N * 2, false},
                       {"y", d_y, M * N * 2, true},
-                      {"z", d_z, M * N * 2, true},
-                      {"the workspace", d_ws, ws_bytes < need ? 0 : need, true}};
+                      {"z", d_z, M * N * 2, true}};
   if ((st = check_bufs(bufs)) != LQ_OK) return st;
-  if ((st = check_ws(d_ws, ws_bytes, need)) != LQ_OK) return st;
   DenseForward d{};
   d.x = d_x;
   d.w = d_w;
@@ -209,14 +201,10 @@ lq_status lq_dense_linear_bwd(const void* d_dy, const void* d_z, const void* d_x
   return launched(launch_dense_backward(d, s), "dense linear backward launch");
 }
 
-int64_t lq_gated_linear_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return bad_extent(M, N, K) ? -1 : 0;
-}
-
 lq_status lq_gated_linear(const void* d_x, const void* d_wg, const void* d_wu,
                           const void* d_bias_g, const void* d_bias_u, int32_t dtype, int64_t M,
                           int64_t N, int64_t K, int32_t act, void* d_h, void* d_g, void* d_u,
-                          void* d_ws, int64_t ws_bytes, void* stream) {
+                          void* stream) {
   lq_status st = check_dense(dtype, M, N, K, act);
   if (st != LQ_OK) return st;
   if (!d_g != !d_u) {
@@ -225,7 +213,6 @@ lq_status lq_gated_linear(const void* d_x, const void* d_wg, const void* d_wu,
   }
   if (M == 0) return LQ_OK;
   if (!d_x || !d_wg || !d_wu || !d_h) return null_pointer("x, Wg, Wu or h");
-  const int64_t need = lq_gated_linear_workspace_bytes(M, N, K);
   const Buf bufs[] = {{"x", d_x, M * K * 2, false},
                       {"Wg", d_wg, N * K * 2, false},
                       {"Wu", d_wu, N * K * 2, false},
@@ -233,10 +220,8 @@ lq_status lq_gated_linear(const void* d_x, const void* d_wg, const void* d_wu,
                       {"the up bias", d_bias_u, N * 2, false},
                       {"h", d_h, M * N * 2, true},
                       {"g", d_g, M * N * 2, true},
-                      {"u", d_u, M * N * 2, true},
-                      {"the workspace", d_ws, ws_bytes < need ? 0 : need, true}};
+                      {"u", d_u, M * N * 2, true}};
   if ((st = check_bufs(bufs)) != LQ_OK) return st;
-  if ((st = check_ws(d_ws, ws_bytes, need)) != LQ_OK) return st;
   DenseForward d{};
   d.x = d_x;
   d.w = d_wg;

@@ -63,15 +63,12 @@ SIGNATURES = {
     "lq_cta_apply": (_i32, [_vp, _i64, _vp, _i32, _vp, _vp]),
     "lq_cta_stack_workspace_bytes": (_i64, [_pp, _i32, _i64]),
     "lq_loop_stack_cta": (_i32, [_vp, _i32, _i64, _pp, _i32, _i32, _vp, _vp, _vp, _i64, _vp]),
-    "lq_dense_linear_workspace_bytes": (_i64, [_i64, _i64, _i64]),
-    "lq_dense_linear": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp,
-                               _i64, _vp]),
+    "lq_dense_linear": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
     "lq_dense_linear_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64, _i32]),
     "lq_dense_linear_bwd": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp,
                                    _vp, _i32, _i32, _vp, _i64, _vp]),
-    "lq_gated_linear_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "lq_gated_linear": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp,
-                               _vp, _vp, _i64, _vp]),
+                               _vp, _vp]),
     "lq_gated_linear_bwd_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "lq_gated_linear_bwd": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32,
                                    _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _i64, _vp]),
@@ -468,47 +465,48 @@ def _code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _mat(t: Optional[torch.Tensor], name: str, shape, dtype, device: torch.device) -> Optional[int]:
-    """Device pointer of a contiguous tensor of this shape and dtype on this device."""
+def _mat(t: Optional[torch.Tensor], name: str, shape, dtype, dev: int) -> Optional[int]:
+    """Device pointer of a contiguous tensor of this shape and dtype on device dev."""
     if t is None:
         return None
-    if (t.shape != shape or t.dtype != dtype or t.get_device() != device.index
-            or not t.is_contiguous()):
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on "
-                         f"{device}, not {t.dtype} of shape {tuple(t.shape)} on {t.device}"
+                         f"cuda:{dev}, not {t.dtype} of shape {tuple(t.shape)} on {t.device}"
                          + ("" if t.is_contiguous() else " with strides %s" % (t.stride(),)))
     return t.data_ptr()
 
 
-def _on_device(t: torch.Tensor, name: str, dims: int) -> torch.device:
-    if not t.is_cuda:
+def _on_device(t: torch.Tensor, name: str, dims: int) -> int:
+    """Index of the tensor's device, which has to be the current one."""
+    dev = t.get_device()  # -1 on the host
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions")
-    if t.get_device() != torch.cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return t.device
+    return dev
 
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A new tensor that belongs to the stream the call runs on."""
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """A new tensor on like's device that belongs to the stream the call runs on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _scratch(ws: Optional[torch.Tensor], n: int, device, stream):
+def _scratch(ws: Optional[torch.Tensor], n: int, like: torch.Tensor, stream):
     """(pointer, bytes, tensor to keep) of a workspace of n bytes."""
     if n < 0:
         raise ValueError("invalid shape")
     if ws is None:
         if n == 0:
             return None, 0, None
-        ws = _empty(n, torch.uint8, device, stream)
-    elif ws.device != device or not ws.is_contiguous():
+        ws = _empty(n, torch.uint8, like, stream)
+    elif ws.get_device() != like.get_device() or not ws.is_contiguous():
         raise ValueError("the workspace must be contiguous and on the operands' device")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
@@ -516,7 +514,7 @@ def _scratch(ws: Optional[torch.Tensor], n: int, device, stream):
 def lq_dense_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, *,
                     act: int = LQ_ACT_NONE, residual: Optional[torch.Tensor] = None,
                     y: Optional[torch.Tensor] = None, z: Optional[torch.Tensor] = None,
-                    want_z: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+                    want_z: bool = False, stream=None):
     """y = act(x w^T + bias) + residual; returns (y, z), z the pre-activation that
     the backward pass reads (None unless wanted).  x M x K, w N x K, bf16 or f16;
     y may be the residual itself."""
@@ -525,28 +523,27 @@ def lq_dense_linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tenso
     N = w.shape[0]
     dt = x.dtype
     if y is None:
-        y = _empty((M, N), dt, dev, stream)
+        y = _empty((M, N), dt, x, stream)
     if z is None and want_z:
-        z = _empty((M, N), dt, dev, stream)
-    L = _lib or lib()
-    p_ws, n_ws, keep = _scratch(ws, L.lq_dense_linear_workspace_bytes(M, N, K), dev, stream)
-    st = L.lq_dense_linear(
+        z = _empty((M, N), dt, x, stream)
+    st = (_lib or lib()).lq_dense_linear(
         _mat(x, "x", (M, K), dt, dev), _mat(w, "w", (N, K), dt, dev),
         _mat(bias, "bias", (N,), dt, dev), _mat(residual, "residual", (M, N), dt, dev),
         _code(x, "x"), M, N, K, act, _mat(y, "y", (M, N), dt, dev),
-        _mat(z, "z", (M, N), dt, dev), p_ws, n_ws, _stream(stream))
-    _check(st, "lq_dense_linear")
+        _mat(z, "z", (M, N), dt, dev), _stream(stream))
+    if st:
+        _check(st, "lq_dense_linear")
     return y, z
 
 
-def _grad_out(given, want, shape, dtype, dev, stream, accumulate, name):
+def _grad_out(given, want, shape, dtype, like, stream, accumulate, name):
     if given is not None:
         return given
     if not want:
         return None
     if accumulate:
         raise ValueError(f"accumulating needs the {name} to add to")
-    return _empty(shape, dtype, dev, stream)
+    return _empty(shape, dtype, like, stream)
 
 
 def lq_dense_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional[torch.Tensor],
@@ -566,11 +563,11 @@ def lq_dense_linear_bwd(dy: torch.Tensor, x: Optional[torch.Tensor], w: Optional
     dt = dy.dtype
     if g_dtype is None:
         g_dtype = dw.dtype if dw is not None else db.dtype if db is not None else dt
-    dx = _grad_out(dx, want_dx, (M, K), dt, dev, stream, False, "dx")
-    dw = _grad_out(dw, want_dw, (N, K), g_dtype, dev, stream, accumulate, "dw")
-    db = _grad_out(db, want_db, (N,), g_dtype, dev, stream, accumulate, "db")
+    dx = _grad_out(dx, want_dx, (M, K), dt, dy, stream, False, "dx")
+    dw = _grad_out(dw, want_dw, (N, K), g_dtype, dy, stream, accumulate, "dw")
+    db = _grad_out(db, want_db, (N,), g_dtype, dy, stream, accumulate, "db")
     n = lib().lq_dense_linear_bwd_workspace_bytes(M, N, K, act)
-    p_ws, n_ws, keep = _scratch(ws, n, dev, stream)
+    p_ws, n_ws, keep = _scratch(ws, n, dy, stream)
     st = lib().lq_dense_linear_bwd(
         _mat(dy, "dy", (M, N), dt, dev), _mat(z, "z", (M, N), dt, dev),
         _mat(x, "x", (M, K), dt, dev), _mat(w, "w", (N, K), dt, dev), _code(dy, "dy"), M, N, K,
@@ -585,7 +582,7 @@ def lq_gated_linear(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor,
                     bg: Optional[torch.Tensor] = None, bu: Optional[torch.Tensor] = None, *,
                     act: int = LQ_ACT_SILU, h: Optional[torch.Tensor] = None,
                     g: Optional[torch.Tensor] = None, u: Optional[torch.Tensor] = None,
-                    want_gu: bool = False, ws: Optional[torch.Tensor] = None, stream=None):
+                    want_gu: bool = False, stream=None):
     """h = act(x wg^T + bg) * (x wu^T + bu); returns (h, g, u), the two factors
     before the activation where the backward pass will read them (else None)."""
     dev = _on_device(x, "x", 2)
@@ -593,18 +590,18 @@ def lq_gated_linear(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor,
     N = wg.shape[0]
     dt = x.dtype
     if h is None:
-        h = _empty((M, N), dt, dev, stream)
+        h = _empty((M, N), dt, x, stream)
     if want_gu:
-        g = _empty((M, N), dt, dev, stream) if g is None else g
-        u = _empty((M, N), dt, dev, stream) if u is None else u
-    p_ws, n_ws, keep = _scratch(ws, lib().lq_gated_linear_workspace_bytes(M, N, K), dev, stream)
-    st = lib().lq_gated_linear(
+        g = _empty((M, N), dt, x, stream) if g is None else g
+        u = _empty((M, N), dt, x, stream) if u is None else u
+    st = (_lib or lib()).lq_gated_linear(
         _mat(x, "x", (M, K), dt, dev), _mat(wg, "wg", (N, K), dt, dev),
         _mat(wu, "wu", (N, K), dt, dev), _mat(bg, "bg", (N,), dt, dev),
         _mat(bu, "bu", (N,), dt, dev), _code(x, "x"), M, N, K, act,
         _mat(h, "h", (M, N), dt, dev), _mat(g, "g", (M, N), dt, dev),
-        _mat(u, "u", (M, N), dt, dev), p_ws, n_ws, _stream(stream))
-    _check(st, "lq_gated_linear")
+        _mat(u, "u", (M, N), dt, dev), _stream(stream))
+    if st:
+        _check(st, "lq_gated_linear")
     return h, g, u
 
 
@@ -627,13 +624,13 @@ def lq_gated_linear_bwd(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor,
     dt = dh.dtype
     if g_dtype is None:
         g_dtype = next((t.dtype for t in (dwg, dwu, dbg, dbu) if t is not None), dt)
-    dx = _grad_out(dx, want_dx, (M, K), dt, dev, stream, False, "dx")
-    dwg = _grad_out(dwg, want_dw, (N, K), g_dtype, dev, stream, accumulate, "dwg")
-    dwu = _grad_out(dwu, want_dw, (N, K), g_dtype, dev, stream, accumulate, "dwu")
-    dbg = _grad_out(dbg, want_db, (N,), g_dtype, dev, stream, accumulate, "dbg")
-    dbu = _grad_out(dbu, want_db, (N,), g_dtype, dev, stream, accumulate, "dbu")
+    dx = _grad_out(dx, want_dx, (M, K), dt, dh, stream, False, "dx")
+    dwg = _grad_out(dwg, want_dw, (N, K), g_dtype, dh, stream, accumulate, "dwg")
+    dwu = _grad_out(dwu, want_dw, (N, K), g_dtype, dh, stream, accumulate, "dwu")
+    dbg = _grad_out(dbg, want_db, (N,), g_dtype, dh, stream, accumulate, "dbg")
+    dbu = _grad_out(dbu, want_db, (N,), g_dtype, dh, stream, accumulate, "dbu")
     n = lib().lq_gated_linear_bwd_workspace_bytes(M, N, K)
-    p_ws, n_ws, keep = _scratch(ws, n, dev, stream)
+    p_ws, n_ws, keep = _scratch(ws, n, dh, stream)
     st = lib().lq_gated_linear_bwd(
         _mat(dh, "dh", (M, N), dt, dev), _mat(g, "g", (M, N), dt, dev),
         _mat(u, "u", (M, N), dt, dev), _mat(x, "x", (M, K), dt, dev),
@@ -662,18 +659,19 @@ def lq_distill_loss(logits: torch.Tensor, t_values: torch.Tensor, t_index: torch
         raise ValueError("t_index must be int32 or int64")
     k = t_values.shape[-1]
     if loss is None:
-        loss = _empty((M,), torch.float32, dev, stream)
+        loss = _empty((M,), torch.float32, logits, stream)
     if grad is None and want_grad:
-        grad = _empty((M, V), logits.dtype, dev, stream)
+        grad = _empty((M, V), logits.dtype, logits, stream)
     f32 = torch.float32
-    st = lib().lq_distill_loss(
+    st = (_lib or lib()).lq_distill_loss(
         _mat(logits, "logits", (M, V), logits.dtype, dev), _code(logits, "logits"), M, V,
         _mat(t_values, "t_values", (M, k), t_values.dtype, dev), _code(t_values, "t_values"),
         _mat(t_index, "t_index", (M, k), t_index.dtype, dev), t_index.element_size(), k,
         _mat(t_lse, "t_lse", (M,), f32, dev), _mat(weight, "weight", (M,), f32, dev), float(temp),
         _mat(loss, "loss", (M,), f32, dev), _mat(grad, "grad", (M, V), logits.dtype, dev),
         _stream(stream))
-    _check(st, "lq_distill_loss")
+    if st:
+        _check(st, "lq_distill_loss")
     return loss, grad
 
 

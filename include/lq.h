@@ -358,14 +358,11 @@ lq_status lq_trajectory_hessian(const void* d_X, int32_t x_dtype, int64_t M, int
  *   d_y         out M x N;
  *   d_z         out M x N, the pre-activation x W^T + bias that
  *               lq_dense_linear_bwd reads, or NULL.
- *   d_ws        lq_dense_linear_workspace_bytes(M, N, K) bytes (may be NULL
- *               when that is 0).
+ * No workspace.
  */
-int64_t lq_dense_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 lq_status lq_dense_linear(const void* d_x, const void* d_w, const void* d_bias,
                           const void* d_residual, int32_t dtype, int64_t M, int64_t N, int64_t K,
-                          int32_t act, void* d_y, void* d_z, void* d_ws, int64_t ws_bytes,
-                          void* stream);
+                          int32_t act, void* d_y, void* d_z, void* stream);
 
 /*
  * lq_dense_linear_bwd -- the gradients of lq_dense_linear:
@@ -379,6 +376,8 @@ lq_status lq_dense_linear(const void* d_x, const void* d_w, const void* d_bias,
  *   accumulate  add to what dw and db hold (the gradient of a weight that all
  *               loops share, loop by loop); needs g_dtype LQ_F32
  *               (LQ_ERR_UNSUPPORTED).
+ *   d_ws        lq_dense_linear_bwd_workspace_bytes(M, N, K, act) bytes (dz and
+ *               partial column sums); scratch.
  * dz is rounded to dtype before the products (the tensor cores' operand
  * type); db sums the float32 values.
  */
@@ -396,12 +395,12 @@ lq_status lq_dense_linear_bwd(const void* d_dy, const void* d_z, const void* d_x
  *   d_bias_g, d_bias_u  N values each, or NULL;
  *   d_h         out M x N;
  *   d_g, d_u    out M x N, what lq_gated_linear_bwd reads; both or neither.
+ * No workspace.
  */
-int64_t lq_gated_linear_workspace_bytes(int64_t M, int64_t N, int64_t K);
 lq_status lq_gated_linear(const void* d_x, const void* d_wg, const void* d_wu,
                           const void* d_bias_g, const void* d_bias_u, int32_t dtype, int64_t M,
                           int64_t N, int64_t K, int32_t act, void* d_h, void* d_g, void* d_u,
-                          void* d_ws, int64_t ws_bytes, void* stream);
+                          void* stream);
 
 /*
  * lq_gated_linear_bwd -- the gradients of lq_gated_linear:

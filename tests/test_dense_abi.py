@@ -18,7 +18,7 @@ def L():
 
 
 def dense(L, x=X, w=W, b=None, r=None, dt=lq.LQ_BF16, M=4, N=8, K=16, act=0, y=Y, z=None):
-    return L.lq_dense_linear(x, w, b, r, dt, M, N, K, act, y, z, WS, BIG, None)
+    return L.lq_dense_linear(x, w, b, r, dt, M, N, K, act, y, z, None)
 
 
 def dense_bwd(L, dy=X, z=None, x=W, w=Z, dt=lq.LQ_BF16, M=4, N=8, K=16, act=0, dx=Y, dw=R,
@@ -55,7 +55,7 @@ def test_dense_linear_refusals(L):
 
 def test_gated_linear_refusals(L):
     def gated(x=X, wg=W, wu=R, dt=lq.LQ_F16, M=4, N=8, K=16, act=2, h=Y, g=None, u=None, b=None):
-        return L.lq_gated_linear(x, wg, wu, b, b, dt, M, N, K, act, h, g, u, WS, BIG, None)
+        return L.lq_gated_linear(x, wg, wu, b, b, dt, M, N, K, act, h, g, u, None)
 
     assert gated(dt=lq.LQ_F32) == lq.LQ_ERR_UNSUPPORTED
     assert gated(K=20) == lq.LQ_ERR_SHAPE
@@ -97,8 +97,7 @@ def test_backward_refusals(L):
 
 
 def test_workspace_sizes(L):
-    for f in (L.lq_dense_linear_workspace_bytes, L.lq_gated_linear_workspace_bytes,
-              L.lq_gated_linear_bwd_workspace_bytes,
+    for f in (L.lq_gated_linear_bwd_workspace_bytes,
               lambda M, N, K: L.lq_dense_linear_bwd_workspace_bytes(M, N, K, 2)):
         for bad in ((-1, 8, 8), (4, 0, 8), (4, 8, -8), (1 << 31, 8, 8), (1 << 30, 1 << 30, 8)):
             assert f(*bad) == -1
