@@ -21,8 +21,8 @@
 // gradient a second one that finds the row in L2, where the rows in flight (some
 // 100 KB each, four per SM) stay; the gradients are stored as streaming data so
 // as not to displace them.  Nothing limits the row's length, and nothing waits
-// but at barriers.  Measured, 8192 x 49152 bf16 logits: 219 us for the loss
-// (floor 123), 372 with the gradient (floor 246).  Holding the row in shared
+// but at barriers.  Measured, 8192 x 49152 bf16 logits: 209 us for the loss
+// (floor 123), 355 with the gradient (floor 246).  Holding the row in shared
 // memory between the passes (bulk copies in and out, two rows per SM) took 250
 // and 342-365, and 46-56 against 26 for the loss of 255 x 100003 float32 logits;
 // a ring of bulk copies running ahead across passes and rows took 600, and keeping
@@ -43,10 +43,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kMaxSmem = 164 * 1024;  // 64 KB of bitmap, 96 KB of listed entries
-constexpr int kUnroll = 4;  // 16-byte loads of a thread's batch
-constexpr int kBigThreads = 256;
 constexpr int kMaxCluster = 8;
-constexpr size_t kSmallSlice = 32 * 1024;  // bytes of a slice up to which 128 threads take it
 constexpr float kNegInf = -INFINITY;
 
 template <typename T>
@@ -165,6 +162,7 @@ struct DistillParams {
   int64_t M, V;
   int k, t_dtype, idx64;
   int slice;   // elements per CTA, a multiple of 32
+  int ahead;   // several rows per resident CTA: fetch a row's rest to L2 at once
   float temp, inv_temp;
   double c2d;  // log2(e) / temp
   float c2;    // the same, rounded: the student's exponents, and consistently its
@@ -256,8 +254,8 @@ struct Slice {
   }
 };
 
-template <typename T, bool kTail, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads)
+template <typename T, bool kTail, int kThreads, int kUnroll, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas)
     k_distill(const __grid_constant__ DistillParams P) {
   constexpr int kE = Log<T>::kE, kWarps = kThreads / 32;
   extern __shared__ uint32_t bits[];  // the slice's listed entries
@@ -307,6 +305,15 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   const float w = P.weight ? P.weight[row] : 1.f;
   uint4 x[kUnroll];
   batch(x, 0);
+  // with many rows, the rest of the slice towards L2 at once: more of it travels
+  // than the loads of the pass alone would ask for (8192 x 49152: 372 -> 355 us;
+  // where all rows are in flight anyway it costs 5 %)
+  if (P.ahead && warp == 0 && n_batch > 1 && elect_one()) {
+    const uint4* p = reinterpret_cast<const uint4*>(zs) + sl.v_lo + kUnroll * kThreads;
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p),
+                 "r"((uint32_t)(n_vec - kUnroll * kThreads) * 16u)
+                 : "memory");
+  }
   bool any = false;
   for (int i0 = tid; i0 < P.k; i0 += 4 * kThreads) {
     int64_t v[4];
@@ -609,9 +616,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads)
   }
 }
 
-template <typename T, bool kTail, int kThreads>
+template <typename T, bool kTail, int kThreads, int kUnroll, int kCtas>
 cudaError_t run(const DistillParams& P, int parts, cudaStream_t s) {
-  auto* k = k_distill<T, kTail, kThreads>;
+  auto* k = k_distill<T, kTail, kThreads, kUnroll, kCtas>;
   const size_t smem = P.slice / 8 + (size_t)P.k * 12;
   static std::atomic<uint64_t> smem_set{0};  // one bit per device
   int dev = 0;
@@ -638,14 +645,22 @@ cudaError_t run(const DistillParams& P, int parts, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, k, P);
 }
 
+template <typename T, bool kTail>
+cudaError_t run_size(const DistillParams& P, int parts, cudaStream_t s) {
+  // Threads and loads in flight by the length of a slice: a short row is all
+  // latency, and small CTAs put more rows on an SM at once (4000 rows of 1003 bf16
+  // logits with gradient: 70 us with 512 threads, 25 with 128, 16 with 64 and half the
+  // loads in flight; 1000 rows of 8001 float32: 17 with that, 14 with 128 and all of
+  // them).
+  const size_t bytes = P.slice * sizeof(T);
+  if (bytes <= 8 * 1024) return run<T, kTail, 64, 2, 20>(P, parts, s);
+  if (bytes <= 32 * 1024) return run<T, kTail, 128, 4, 8>(P, parts, s);
+  return run<T, kTail, 256, 4, 4>(P, parts, s);
+}
+
 template <typename T>
 cudaError_t run_tail(const DistillParams& P, int parts, cudaStream_t s) {
-  // Threads by the length of a slice: a short row is all latency, and small CTAs
-  // put more rows on an SM at once.
-  const bool small = P.slice * sizeof(T) <= kSmallSlice;
-  if (P.t_lse)
-    return small ? run<T, true, 128>(P, parts, s) : run<T, true, kBigThreads>(P, parts, s);
-  return small ? run<T, false, 128>(P, parts, s) : run<T, false, kBigThreads>(P, parts, s);
+  return P.t_lse ? run_size<T, true>(P, parts, s) : run_size<T, false>(P, parts, s);
 }
 
 }  // namespace
@@ -672,6 +687,7 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
   P.t_dtype = a.t_dtype;
   P.idx64 = a.idx64;
   P.slice = (int)slice_of(parts);
+  P.ahead = a.M * parts > 8 * num_sms();
   P.temp = a.temp;
   P.inv_temp = 1.f / a.temp;
   P.c2d = 1.4426950408889634 / (double)a.temp;
