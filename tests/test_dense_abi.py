@@ -72,20 +72,20 @@ def test_backward_refusals(L):
     assert dense_bwd(L, act=lq.LQ_ACT_SILU) == lq.LQ_ERR_ARG  # z missing
     for kw in (dict(dy=None), dict(x=None), dict(w=None)):
         assert dense_bwd(L, **kw) == lq.LQ_ERR_ARG
-    need = L.lq_dense_linear_bwd_workspace_bytes(4, 8, 16, lq.LQ_ACT_SILU)
+    need = L.lq_dense_linear_bwd_workspace_bytes(40, 8, 16, lq.LQ_ACT_SILU)
     assert need > 0 and need % 256 == 0
-    assert dense_bwd(L, z=5 << 44, act=2, n=need - 1) == lq.LQ_ERR_WORKSPACE
-    assert dense_bwd(L, z=5 << 44, act=2, ws=None) == lq.LQ_ERR_ARG
-    assert dense_bwd(L, z=5 << 44, act=2, ws=WS + 16) == lq.LQ_ERR_ALIGN
+    assert dense_bwd(L, M=40, z=5 << 44, act=2, n=need - 1) == lq.LQ_ERR_WORKSPACE
+    assert dense_bwd(L, M=40, z=5 << 44, act=2, ws=None) == lq.LQ_ERR_ARG
+    assert dense_bwd(L, M=40, z=5 << 44, act=2, ws=WS + 16) == lq.LQ_ERR_ALIGN
     for kw in (dict(dx=X), dict(dw=Y), dict(db=Z), dict(dx=WS), dict(dw=WS)):
-        assert dense_bwd(L, **kw) == lq.LQ_ERR_ARG, kw
+        assert dense_bwd(L, M=40, **kw) == lq.LQ_ERR_ARG, kw
     # nothing wanted, or no rows to add: nothing is enqueued
     assert dense_bwd(L, dx=None, dw=None) == lq.LQ_OK
     assert dense_bwd(L, M=0, dy=None, x=None, acc=1, g=lq.LQ_F32, ws=None, n=0) == lq.LQ_OK
 
     def gated_bwd(dh=X, g=1 << 45, u=2 << 45, x=3 << 45, wg=4 << 45, wu=5 << 45, dx=6 << 45,
                   dwg=7 << 45, dwu=8 << 45, gd=lq.LQ_BF16, acc=0, n=BIG):
-        return L.lq_gated_linear_bwd(dh, g, u, x, wg, wu, lq.LQ_BF16, 4, 8, 16, 2, dx, dwg, dwu,
+        return L.lq_gated_linear_bwd(dh, g, u, x, wg, wu, lq.LQ_BF16, 40, 8, 16, 2, dx, dwg, dwu,
                                      None, None, gd, acc, WS, n, None)
 
     for kw in (dict(dh=None), dict(g=None), dict(u=None), dict(wg=None), dict(wu=None),
@@ -104,7 +104,9 @@ def test_workspace_sizes(L):
         for ok in ((0, 1, 8), (1, 1, 8), (4096, 5632, 2048)):
             n = f(*ok)
             assert n >= 0 and n % 256 == 0
-    # an aligned output gradient without an activation is used as it is
+    # a few rows need none; an aligned output gradient without an activation is
+    # used as it is
+    assert L.lq_gated_linear_bwd_workspace_bytes(4, 5632, 2048) == 0
     assert L.lq_dense_linear_bwd_workspace_bytes(4096, 2048, 2048, 0) < 4096 * 2048
     assert L.lq_dense_linear_bwd_workspace_bytes(4096, 2047, 2048, 0) >= 4096 * 2047 * 2
     assert L.lq_gated_linear_bwd_workspace_bytes(4096, 2048, 64) >= 4096 * 2048 * 4

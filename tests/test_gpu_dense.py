@@ -160,7 +160,7 @@ def check_gated_bwd(M, N, K, dt, act, g_dtype=None, seed=0):
           f * du.abs().sum(0), "dbu")
 
 
-SHAPES = [(1, 8, 8), (1, 1, 8), (2, 3, 24), (7, 65, 72), (8, 256, 256), (9, 255, 264),
+SHAPES = [(1, 8, 8), (1, 1, 8), (2, 3, 24), (3, 1000, 520), (4, 257, 264), (7, 65, 72), (8, 256, 256), (9, 255, 264),
           (16, 1000, 1032), (17, 64, 64), (33, 1, 8), (127, 128, 128), (128, 130, 40),
           (129, 257, 200), (300, 1000, 520), (1000, 264, 2048), (513, 2049, 256),
           (2300, 640, 72), (1, 2048, 5632), (13, 5632, 2048)]
@@ -474,7 +474,7 @@ def test_refusals():
         lq.lq_dense_linear(buf.view(-1)[4:4 + 64].view(4, 16), w)
     assert e.value.status == lq.LQ_ERR_ALIGN
     with pytest.raises(lq.LQError) as e:
-        lq.lq_dense_linear_bwd(normal(3, 4, 8, dtype=dt), x, w, normal(3, 4, 8, dtype=dt),
-                               act=lq.LQ_ACT_SILU,
+        lq.lq_dense_linear_bwd(normal(3, 40, 8, dtype=dt), normal(1, 40, 16, dtype=dt), w,
+                               normal(3, 40, 8, dtype=dt), act=lq.LQ_ACT_SILU,
                                ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == lq.LQ_ERR_WORKSPACE
