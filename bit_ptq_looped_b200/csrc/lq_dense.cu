@@ -353,6 +353,8 @@ struct GemmParams {
   int64_t M, N;    // extents of the output (N per factor when gated)
   int64_t ldo;     // elements between output rows
   int n_kb, n_kb1; // contraction blocks; those of the first operand pair
+  int slice_kb;    // blocks of a slice of the contraction (blockIdx.y), n_kb when whole
+  int64_t slice_bytes;  // bytes from one slice's output to the next
   int act;
   int accumulate;
   int vec;         // rows are 16-byte aligned: 16-byte stores
@@ -593,6 +595,7 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
   const int n_tiles = tm * tn;
   const int rank = kPair == 1 ? 0 : (int)cluster_rank();
   const int t_first = blockIdx.x / kPair, t_step = gridDim.x / kPair;
+  const int kb_first = blockIdx.y * P.slice_kb, kb_end = min(P.n_kb, kb_first + P.slice_kb);
 
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -627,7 +630,7 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
         tile_at(t, tm, tn, im, in);
         const int m0 = im * kTileM + rank * BM;
         const int n0 = in * kTileN + (kEpi == kEpiGated ? 0 : rank * (kBN / kPair));
-        for (int kb = 0; kb < P.n_kb; ++kb, ++it) {
+        for (int kb = kb_first; kb < kb_end; ++kb, ++it) {
           if (!wait_bounded(bar_empty + 8 * st, ph, abort_flag)) {
             ok = false;
             break;
@@ -684,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
         if (!wait_bounded(bar_acce + 8 * buf, ((uint32_t)(j >> 1) & 1u) ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(buf * kBN);
-        for (int kb = 0; kb < P.n_kb; ++kb) {
+        for (int kb = kb_first; kb < kb_end; ++kb) {
           if (!wait_bounded(bar_full + 8 * st, ph, abort_flag)) {
             ok = false;
             break;
@@ -694,7 +697,8 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
           const uint64_t db = descB + (uint64_t)(st * (C::kStageB >> 4));
 #pragma unroll
           for (int i = 0; i < BK / 16; ++i)
-            umma_f16<kPair>(d, da + stepA * i, db + stepB * i, idesc, (kb | i) ? 1u : 0u);
+            umma_f16<kPair>(d, da + stepA * i, db + stepB * i, idesc,
+                            (kb != kb_first || i != 0) ? 1u : 0u);
           commit_all<kPair>(bar_empty + 8 * st);
           if (++st == C::kStages) st = 0, ph ^= 1u;
         }
@@ -740,8 +744,8 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
       tc_fence_after();
       const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) +
                            (uint32_t)(buf * kBN + part * C::kCols);
-      const RowMap map = {P.M,          P.rows1,       P.split,
-                          (char*)P.out, (char*)P.out2, P.ldo * (kEpi == kEpiF32 ? 4 : 2)};
+      const RowMap map = {P.M, P.rows1, P.split, (char*)P.out + blockIdx.y * P.slice_bytes,
+                          (char*)P.out2, P.ldo * (kEpi == kEpiF32 ? 4 : 2)};
       for (int u = 0; u < C::kCols; u += C::kUnit) {
         const int64_t col = n0 + u;
         if (!live || col >= P.N) continue;
@@ -1102,6 +1106,38 @@ __global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ sums
     ((uint16_t*)o)[i] = Elem<T>::round(s);
 }
 
+// the slices of a product added up, in order: rows x cols float32 each, to
+// float32 (added to what is there) or rounded; rows as in GemmParams
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_add_slices(const float* __restrict__ part, int slices, int64_t rows, int64_t cols,
+                 const GemmParams P, int f32) {
+  pdl_trigger();
+  pdl_wait();
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;  // cols is a multiple of 8
+  if (i >= rows * cols) return;
+  const int64_t r = i / cols, c = i - r * cols;
+  const RowMap map = {P.M, P.rows1, P.split, (char*)P.out, (char*)P.out2, cols * (f32 ? 4 : 2)};
+  char* dst = map(r);
+  if (!dst) return;
+  float4 v = *reinterpret_cast<const float4*>(part + i);
+  for (int k = 1; k < slices; ++k) {
+    const float4 q = *reinterpret_cast<const float4*>(part + k * rows * cols + i);
+    v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+  }
+  if (f32) {
+    float4* o = reinterpret_cast<float4*>(dst + c * 4);
+    if (P.accumulate) {
+      const float4 q = *o;
+      v.x += q.x, v.y += q.y, v.z += q.z, v.w += q.w;
+    }
+    *o = v;
+  } else {
+    *reinterpret_cast<uint2*>(dst + c * 2) =
+        make_uint2(Elem<T>::pack(v.x, v.y), Elem<T>::pack(v.z, v.w));
+  }
+}
+
 // ---------------------------------------------------------------------------
 // backward pass of up to 4 rows: stream the weights once for dx, write the
 // weights' gradients once, dz in float32 throughout.  Measured at 5632 x 2048 (dx
@@ -1366,7 +1402,7 @@ bool operand_map(CUtensorMap* m, const Operand& o, bool mn, bool bf16, int tile_
 
 template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi>
 cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
-                     const GemmParams& P, cudaStream_t s) {
+                     const GemmParams& P, int slices, cudaStream_t s) {
   using C = Cfg<kBN, kPair, kEpi>;
   constexpr bool bf16 = Elem<T>::kFormat == 1;
   constexpr int rowsB = kEpi == kEpiGated ? kBN / 2 : kBN / kPair;
@@ -1392,7 +1428,8 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
   const int64_t tiles = ((P.M + kTileM - 1) / kTileM) * ((P.N + kTileN - 1) / kTileN);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, num_sms() / kPair) * kPair));
+  const int64_t slots = std::max(1, num_sms() / kPair / slices);
+  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, slots) * kPair), (unsigned)slices);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -1415,23 +1452,51 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
 // 34.7, 38.9 and 56.2 us; on 16384 x 5632 x 2048: 251, 281, 331 and 466; on
 // 128 x 2048 x 2048: 14.2, 9.1, 8.9 and 8.2; on 2048 x 256 x 256: 6.4, 5.0, 4.5
 // and 4.2.
-template <typename T, bool kAMn, bool kBMn, int kEpi>
-cudaError_t pick_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
-                      const GemmParams& P, cudaStream_t s) {
-  constexpr int f = kEpi == kEpiGated ? 2 : 1;
-  auto clocks = [&](int bm, int bn, int slots, int64_t per_block, int64_t once) {
-    const int64_t tiles = ((P.M + bm - 1) / bm) * ((P.N * f + bn - 1) / bn);
-    return (tiles + slots - 1) / slots * P.n_kb * per_block + once;
-  };
+// A long contraction over few tiles is cut into slices (only where the caller has
+// room for their float32 outputs, which another pass adds up): that pass, with its
+// launch on the host, and the slices' outputs count as well, at 6000 clocks and
+// 2600 bytes a clock.  dw of 8192 x 512 x 512 25 -> 17 us, dx of 64 x 5632 x 2048
+// gated 30 -> 17 us.
+struct Shape {
+  int tile, slices;
+  int64_t clocks;
+};
+Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices) {
   const int sms = num_sms();
-  const int64_t c2256 = clocks(256, 256, sms / 2, 512, 7800),
-                c2128 = clocks(256, 128, sms / 2, 300, 4300),
-                c128 = clocks(128, 128, sms, 330, 3000), c64 = clocks(128, 64, sms, 285, 2600);
-  const int64_t best = std::min(std::min(c2256, c2128), std::min(c128, c64));
-  if (best == c2256) return run_gemm<T, 256, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
-  if (best == c2128) return run_gemm<T, 128, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
-  if (best == c128) return run_gemm<T, 128, 1, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
-  return run_gemm<T, 64, 1, kAMn, kBMn, kEpi>(a, a2, b, b2, P, s);
+  struct Kind {
+    int tile, bm, bn, slots, per_block, once;
+  };
+  const Kind kinds[4] = {{2256, 256, 256, sms / 2, 512, 7800},
+                         {2128, 256, 128, sms / 2, 300, 4300},
+                         {128, 128, 128, sms, 330, 3000},
+                         {64, 128, 64, sms, 285, 2600}};
+  Shape best{2256, 1, INT64_MAX};
+  for (int slices = 1; slices <= max_slices; slices *= 2) {
+    const int kb = (n_kb + slices - 1) / slices;
+    if (slices > 1 && (kb < 8 || (int64_t)(slices - 1) * kb >= n_kb)) break;
+    for (const Kind& k : kinds) {
+      const int64_t tiles = ((M + k.bm - 1) / k.bm) * ((N * factors + k.bn - 1) / k.bn) * slices;
+      int64_t c = (tiles + k.slots - 1) / k.slots * kb * k.per_block + k.once;
+      if (slices > 1) c += 6000 + M * N * 8 * slices / 2600;
+      if (c < best.clocks) best = {k.tile, slices, c};
+    }
+  }
+  return best;
+}
+
+template <typename T, bool kAMn, bool kBMn, int kEpi>
+cudaError_t run_shape(const Shape& sh, const Operand& a, const Operand& a2, const Operand& b,
+                      const Operand& b2, const GemmParams& P, cudaStream_t s) {
+  switch (sh.tile) {
+    case 2256:
+      return run_gemm<T, 256, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, sh.slices, s);
+    case 2128:
+      return run_gemm<T, 128, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, sh.slices, s);
+    case 128:
+      return run_gemm<T, 128, 1, kAMn, kBMn, kEpi>(a, a2, b, b2, P, sh.slices, s);
+    default:
+      return run_gemm<T, 64, 1, kAMn, kBMn, kEpi>(a, a2, b, b2, P, sh.slices, s);
+  }
 }
 
 GemmParams base_params(int64_t M, int64_t N, int64_t kdim) {
@@ -1439,7 +1504,7 @@ GemmParams base_params(int64_t M, int64_t N, int64_t kdim) {
   P.M = M;
   P.N = N;
   P.ldo = N;
-  P.n_kb = P.n_kb1 = (int)((kdim + BK - 1) / BK);
+  P.n_kb = P.n_kb1 = P.slice_kb = (int)((kdim + BK - 1) / BK);
   P.rows1 = P.split = M;
   P.vec = N % 8 == 0;
   return P;
@@ -1477,9 +1542,11 @@ cudaError_t forward(const DenseForward& d, cudaStream_t s) {
   const Operand x{d.x, d.M, d.K, d.K}, w{d.w, d.N, d.K, d.K};
   if (gated) {
     const Operand w2{d.w2, d.N, d.K, d.K};
-    return pick_gemm<T, false, false, kEpiGated>(x, x, w, w2, P, s);
+    return run_shape<T, false, false, kEpiGated>(pick_shape(d.M, d.N, P.n_kb, 2, 1), x, x, w, w2, P,
+                                                 s);
   }
-  return pick_gemm<T, false, false, kEpiDense>(x, x, w, w, P, s);
+  return run_shape<T, false, false, kEpiDense>(pick_shape(d.M, d.N, P.n_kb, 1, 1), x, x, w, w, P,
+                                               s);
 }
 
 template <typename T, bool kWhole, bool kGated>
@@ -1499,9 +1566,39 @@ cudaError_t act_grad_launch(const GradParams& P, dim3 grid, cudaStream_t s) {
   }
 }
 
+// A backward product, in slices where its shape says so.
+template <typename T, bool kAMn, bool kBMn>
+cudaError_t run_grad(const Shape& sh, const Operand& a, const Operand& a2, const Operand& b,
+                     const Operand& b2, const GemmParams& P, bool f32, float* part,
+                     cudaStream_t s) {
+  if (sh.slices == 1)
+    return f32 ? run_shape<T, kAMn, kBMn, kEpiF32>(sh, a, a2, b, b2, P, s)
+               : run_shape<T, kAMn, kBMn, kEpiStore>(sh, a, a2, b, b2, P, s);
+  GemmParams Q = P;
+  Q.out = part;
+  Q.out2 = nullptr;
+  Q.rows1 = Q.split = P.M;
+  Q.accumulate = 0;
+  Q.slice_kb = (P.n_kb + sh.slices - 1) / sh.slices;
+  Q.slice_bytes = P.M * P.N * 4;
+  cudaError_t e = run_shape<T, kAMn, kBMn, kEpiF32>(sh, a, a2, b, b2, Q, s);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(k_add_slices<T>, dim3((unsigned)((P.M * P.N / 4 + 255) / 256)), dim3(256), 0,
+                       s, true, (const float*)part, sh.slices, P.M, P.N, P, f32 ? 1 : 0);
+}
+
 // few rows: the grid's second dimension counts 64-row pieces of the weights
 bool bwd_by_rows(int64_t M, int64_t N) {
   return M <= kBwdRowsMax && N <= 65535 * (int64_t)kBwdRows;
+}
+
+// shapes of the backward products (half: columns of dz of one factor)
+constexpr int kMaxSlices = 8;
+Shape dx_shape(int64_t M, int64_t half, int64_t K, bool gated) {
+  return pick_shape(M, K, (int)((half + BK - 1) / BK) * (gated ? 2 : 1), 1, kMaxSlices);
+}
+Shape dw_shape(int64_t rows, int64_t K, int64_t M) {
+  return pick_shape(rows, K, (int)((M + BK - 1) / BK), 1, kMaxSlices);
 }
 
 template <typename T, int kM, bool kGated>
@@ -1534,11 +1631,12 @@ cudaError_t backward(const DenseBackward& d, cudaStream_t s) {
     return gated ? run_rows_bwd<T, kBwdRowsMax, true>(R, s)
                  : run_rows_bwd<T, kBwdRowsMax, false>(R, s);
   }
-  const DenseBwdPlan pl = dense_bwd_plan(d.M, d.N, gated, d.act != LQ_ACT_NONE);
+  const DenseBwdPlan pl = dense_bwd_plan(d.M, d.N, d.K, gated, d.act != LQ_ACT_NONE);
   const bool products = d.dx || d.dw || d.dw2;
   const bool sums = d.db || d.db2;
   uint16_t* dz = (uint16_t*)d.ws;
   float* part = (float*)((char*)d.ws + pl.dz_bytes);
+  float* slices = (float*)((char*)d.ws + pl.dz_bytes + pl.sum_bytes);
   const int nf = gated ? 2 : 1;
   cudaError_t e;
   if (sums || (products && pl.copy)) {
@@ -1583,7 +1681,8 @@ cudaError_t backward(const DenseBackward& d, cudaStream_t s) {
       b2.p = d.w2;
       P.n_kb = 2 * P.n_kb1;
     }
-    e = pick_gemm<T, false, true, kEpiStore>(a, a2, b, b2, P, s);
+    P.slice_kb = P.n_kb;
+    e = run_grad<T, false, true>(dx_shape(d.M, half, d.K, gated), a, a2, b, b2, P, false, slices, s);
     if (e != cudaSuccess) return e;
   }
   if (d.dw || d.dw2) {
@@ -1599,8 +1698,7 @@ cudaError_t backward(const DenseBackward& d, cudaStream_t s) {
     P.accumulate = d.accumulate;
     const Operand a{only2 ? (const void*)(dz + half) : dzp, rows, d.M, pl.ldz};
     const Operand b{d.x, d.K, d.M, d.K};
-    e = d.f32 ? pick_gemm<T, true, true, kEpiF32>(a, a, b, b, P, s)
-              : pick_gemm<T, true, true, kEpiStore>(a, a, b, b, P, s);
+    e = run_grad<T, true, true>(dw_shape(rows, d.K, d.M), a, a, b, b, P, d.f32, slices, s);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
@@ -1612,7 +1710,7 @@ cudaError_t launch_dense_forward(const DenseForward& d, cudaStream_t s) {
   return d.dtype == LQ_BF16 ? forward<__nv_bfloat16>(d, s) : forward<__half>(d, s);
 }
 
-DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, bool gated, bool act) {
+DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, int64_t K, bool gated, bool act) {
   DenseBwdPlan p{};
   if (bwd_by_rows(M, N)) return p;
   // dz is its own matrix where it differs from dy, or where dy's rows do not
@@ -1625,6 +1723,14 @@ DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, bool gated, bool act) {
   p.rows = std::max<int64_t>(64, (M + 255) / 256);
   p.row_blocks = (int)((M + p.rows - 1) / p.rows);
   p.sum_bytes = ((int64_t)p.row_blocks * N * (gated ? 2 : 1) * 4 + 255) / 256 * 256;
+  // the largest of the products' slices (dw of one or of both factors)
+  const int64_t half = gated ? p.ldz / 2 : p.ldz;
+  auto room = [](const Shape& sh, int64_t rows, int64_t cols) {
+    return sh.slices > 1 ? (rows * cols * 4 * sh.slices + 255) / 256 * 256 : 0;
+  };
+  p.slice_bytes = std::max(room(dx_shape(M, half, K, gated), M, K), room(dw_shape(N, K, M), N, K));
+  if (gated)
+    p.slice_bytes = std::max(p.slice_bytes, room(dw_shape(half + N, K, M), half + N, K));
   return p;
 }
 

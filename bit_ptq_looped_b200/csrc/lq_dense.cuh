@@ -31,13 +31,13 @@ struct DenseForward {
 cudaError_t launch_dense_forward(const DenseForward& d, cudaStream_t s);
 
 // workspace layout of a backward call: dz (M x ldz), then the row blocks'
-// partial column sums
+// partial column sums, then the slices of a product cut along its contraction
 struct DenseBwdPlan {
   bool copy;  // dz is written (else dy serves as it is)
-  int64_t ldz, dz_bytes, rows, sum_bytes;
+  int64_t ldz, dz_bytes, rows, sum_bytes, slice_bytes;
   int row_blocks;
 };
-DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, bool gated, bool act);
+DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, int64_t K, bool gated, bool act);
 
 struct DenseBackward {
   const void *dy, *z, *u, *x, *w, *w2;

@@ -113,9 +113,9 @@ lq_status clear(void* p, int64_t bytes, cudaStream_t s) {
   return e == cudaSuccess ? LQ_OK : cuda_error(e, "clear gradient");
 }
 
-int64_t bwd_bytes(int64_t M, int64_t N, bool gated, bool act) {
-  const DenseBwdPlan p = dense_bwd_plan(M, N, gated, act);
-  return p.dz_bytes + p.sum_bytes;
+int64_t bwd_bytes(int64_t M, int64_t N, int64_t K, bool gated, bool act) {
+  const DenseBwdPlan p = dense_bwd_plan(M, N, K, gated, act);
+  return p.dz_bytes + p.sum_bytes + p.slice_bytes;
 }
 
 lq_status launched(cudaError_t e, const char* what) {
@@ -155,7 +155,7 @@ lq_status lq_dense_linear(const void* d_x, const void* d_w, const void* d_bias,
 }
 
 int64_t lq_dense_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t act) {
-  return bad_extent(M, N, K) ? -1 : bwd_bytes(M, N, false, act != LQ_ACT_NONE);
+  return bad_extent(M, N, K) ? -1 : bwd_bytes(M, N, K, false, act != LQ_ACT_NONE);
 }
 
 lq_status lq_dense_linear_bwd(const void* d_dy, const void* d_z, const void* d_x,
@@ -240,7 +240,7 @@ lq_status lq_gated_linear(const void* d_x, const void* d_wg, const void* d_wu,
 }
 
 int64_t lq_gated_linear_bwd_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return bad_extent(M, N, K) ? -1 : bwd_bytes(M, N, true, true);
+  return bad_extent(M, N, K) ? -1 : bwd_bytes(M, N, K, true, true);
 }
 
 lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u,

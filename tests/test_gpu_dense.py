@@ -225,6 +225,11 @@ def test_many_tiles_and_long_contractions():
     check_gated(4200, 2816, 256, torch.bfloat16, lq.LQ_ACT_SILU, False)
     check_dense_bwd(20000, 264, 136, torch.float16, lq.LQ_ACT_RELU)
     check_gated_bwd(9000, 1000, 512, torch.bfloat16, lq.LQ_ACT_SILU)
+    # few tiles: the contraction in slices that another pass adds up
+    check_gated_bwd(8192, 100, 136, torch.bfloat16, lq.LQ_ACT_SILU)
+    check_gated_bwd(8192, 100, 136, torch.float16, lq.LQ_ACT_GELU, g_dtype=torch.float32)
+    check_dense_bwd(33, 5632, 264, torch.bfloat16, lq.LQ_ACT_NONE)
+    check_dense_bwd(70, 5001, 264, torch.bfloat16, lq.LQ_ACT_SILU)
 
 
 @pytest.mark.parametrize("N", [200, 201, 130, 195])
@@ -257,7 +262,7 @@ def test_rows_behind_the_output_stay():
         assert bool((buf[N * K:] == 7).all())
 
 
-@pytest.mark.parametrize("M", [0, 1, 700])
+@pytest.mark.parametrize("M", [0, 1, 700, 8192])
 def test_float32_weight_gradients_accumulate(M):
     """The gradient of a weight shared by the loops, added up loop by loop."""
     dt, N, K = torch.bfloat16, 72, 136
