@@ -26,7 +26,7 @@ NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
     "-Xcompiler", "-fPIC,-O2,-Wall",
-    "-shared", "-cudart", "static",
+    "-shared", "-cudart", "static", "--threads", "8",
 ]
 
 

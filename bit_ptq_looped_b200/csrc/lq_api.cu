@@ -1432,10 +1432,11 @@ lq_status lq_check_device(void* stream) {
   lq_status st = read_and_clear_device_status((cudaStream_t)stream);
   if (st != LQ_OK) return st;
   // bounds-check build: an index a kernel found out of range (none otherwise)
-  const char* files[4] = {"lq_quant.cu", "lq_gemm.cu", "lq_gemv.cu", "lq_cta.cu"};
-  const unsigned long long v[4] = {bounds_fail_quant(), bounds_fail_gemm(), bounds_fail_gemv(),
-                                   bounds_fail_cta()};
-  for (int i = 0; i < 4; ++i)
+  const char* files[6] = {"lq_quant.cu", "lq_gemm.cu",  "lq_gemv.cu",
+                          "lq_cta.cu",   "lq_dense.cu", "lq_distill.cu"};
+  const unsigned long long v[6] = {bounds_fail_quant(), bounds_fail_gemm(),  bounds_fail_gemv(),
+                                   bounds_fail_cta(),   bounds_fail_dense(), bounds_fail_distill()};
+  for (int i = 0; i < 6; ++i)
     if (v[i]) {
       set_error("index out of range in %s line %llu (index %lld)", files[i], v[i] >> 40,
                 (long long)(v[i] & 0xFFFFFFFFFFull));

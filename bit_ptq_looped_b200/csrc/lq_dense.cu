@@ -457,7 +457,7 @@ __device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, c
       const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
       char* dst = map(row0 + row);
       const int64_t c = col0 + pc * kPer;
-      if (dst && c < N)
+      if (dst && c < N && LQ_IN_RANGE(c + kPer - 1, N))
         *reinterpret_cast<uint4*>(dst + c * kEsz) =
             *reinterpret_cast<const uint4*>(stg + piece_at<kRowBytes>(row, pc));
     }
@@ -480,14 +480,15 @@ __device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, c
       const uint4 x = *reinterpret_cast<const uint4*>(stg + piece_at<kRowBytes>(row, pc));
       const uint4 y = *reinterpret_cast<const uint4*>(
           stg + piece_at<kRowBytes>(row, min(pc + 1, kPieces - 1)));
-      if (s0 == 0 || pc < kPieces - 1)
+      if ((s0 == 0 || pc < kPieces - 1) && LQ_IN_RANGE(col0 + s0 + 8 * pc + 7, N))
         *reinterpret_cast<uint4*>(d + s0 + 8 * pc) = shift8(x, y, s0);
       if (s0 != 0) {
 #pragma unroll
         for (int h = 0; h < 8; h += kPieces) {
           const int e = pc + h < s0 ? pc + h : 2 * kWords - 8 + pc + h;
-          d[e] = *reinterpret_cast<const uint16_t*>(stg + piece_at<kRowBytes>(row, e / 8) +
-                                                    (e % 8) * 2);
+          if (LQ_IN_RANGE(col0 + e, N))
+            d[e] = *reinterpret_cast<const uint16_t*>(stg + piece_at<kRowBytes>(row, e / 8) +
+                                                      (e % 8) * 2);
         }
       }
     }
@@ -999,7 +1000,7 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_dense_rows(const RowsParams
     } else if (P.res) {
       v[0] += Elem<T>::load(P.res + o);
     }
-    P.y[o] = Elem<T>::round(v[0]);
+    if (LQ_IN_RANGE(o, (int64_t)P.M * P.N)) P.y[o] = Elem<T>::round(v[0]);
   }
 }
 
@@ -1093,7 +1094,7 @@ __global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
             w.y = Elem<T>::pack(o[f][2], o[f][3]);
             w.z = Elem<T>::pack(o[f][4], o[f][5]);
             w.w = Elem<T>::pack(o[f][6], o[f][7]);
-            *reinterpret_cast<uint4*>(dst) = w;
+            if (LQ_IN_RANGE(dst + 7 - P.dz, P.M * P.ldz)) *reinterpret_cast<uint4*>(dst) = w;
           }
         }
       }
@@ -1309,7 +1310,8 @@ __global__ void __launch_bounds__(256) __cluster_dims__(kBwdSplit, 1, 1)
     if (m >= P.M || col0 + k >= P.K) continue;
     float v = 0.f;
     for (int r = 0; r < kBwdSplit; ++r) v += *cluster.map_shared_rank(&part[0][m][k], r);
-    P.dx[(int64_t)m * P.K + col0 + k] = Elem<T>::round(v);
+    const int64_t at = (int64_t)m * P.K + col0 + k;
+    if (LQ_IN_RANGE(at, (int64_t)P.M * P.K)) P.dx[at] = Elem<T>::round(v);
   }
   cluster.sync();  // no CTA leaves while its sums are read
 }
@@ -1366,6 +1368,7 @@ __global__ void __launch_bounds__(256) k_rows_dw(const RowsBwdParams P) {
         for (int e = 0; e < 8; ++e) v[e] = fmaf(g, xf[e], v[e]);
       }
       const int64_t at = (int64_t)n * P.K + c;
+      if (!LQ_IN_RANGE(at + 7, (int64_t)P.N * P.K)) continue;
       if (P.f32) {
         float4* o = reinterpret_cast<float4*>((float*)dw + at);
 #pragma unroll
@@ -1767,6 +1770,8 @@ DenseBwdPlan dense_bwd_plan(int64_t M, int64_t N, int64_t K, bool gated, bool ac
 cudaError_t launch_dense_backward(const DenseBackward& d, cudaStream_t s) {
   return d.dtype == LQ_BF16 ? backward<__nv_bfloat16>(d, s) : backward<__half>(d, s);
 }
+
+unsigned long long bounds_fail_dense() { return lq_take_bounds_fail(); }
 
 int take_dense_status() {
   int v = 0, zero = 0;

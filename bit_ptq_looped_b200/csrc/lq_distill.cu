@@ -557,7 +557,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       uint4* o = out + b * (kUnroll * kThreads);
       if (b < n_full) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) __stcs(o + u * kThreads, grad(x[u]));
+        for (int u = 0; u < kUnroll; ++u)
+          if (LQ_IN_RANGE(tid + (b * kUnroll + u) * kThreads, n_vec))
+            __stcs(o + u * kThreads, grad(x[u]));
       } else {
         const int left = n_vec - tid - b * (kUnroll * kThreads);
 #pragma unroll
@@ -586,7 +588,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       part = fmaf(p, (float)(a - ((double)z * (double)P.c2 - (double)n.m2)), part);
       mass += p;
     }
-    if (gs) Log<T>::put(gs + e, n.f_top * ex2(fmaf(z, P.c2, -n.m2)) - scale * p);
+    if (gs && LQ_IN_RANGE(sl.c0 + e, P.V))
+      Log<T>::put(gs + e, n.f_top * ex2(fmaf(z, P.c2, -n.m2)) - scale * p);
   });
   {
     const float pf = warp_sum(part), mf = warp_sum(mass);
@@ -664,6 +667,8 @@ cudaError_t run_tail(const DistillParams& P, int parts, cudaStream_t s) {
 }
 
 }  // namespace
+
+unsigned long long bounds_fail_distill() { return lq_take_bounds_fail(); }
 
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s) {
   const int64_t esz = a.dtype == LQ_F32 ? 4 : 2;
