@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "lq_common.cuh"
+#include "lq_dense.cuh"
 
 namespace lq {
 
@@ -1430,7 +1431,12 @@ lq_status lq_check_device(void* stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "pending CUDA error");
   lq_status st = read_and_clear_device_status((cudaStream_t)stream);
+  const int dense = take_dense_status();  // one report covers all status words
   if (st != LQ_OK) return st;
+  if (dense != 0) {
+    set_error("a bounded device-side wait expired in a dense kernel (status %d)", dense);
+    return (lq_status)dense;
+  }
   // bounds-check build: an index a kernel found out of range (none otherwise)
   const char* files[6] = {"lq_quant.cu", "lq_gemm.cu",  "lq_gemv.cu",
                           "lq_cta.cu",   "lq_dense.cu", "lq_distill.cu"};

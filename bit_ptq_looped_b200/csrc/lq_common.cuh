@@ -144,8 +144,6 @@ unsigned long long bounds_fail_quant();
 unsigned long long bounds_fail_gemm();
 unsigned long long bounds_fail_gemv();
 unsigned long long bounds_fail_cta();
-unsigned long long bounds_fail_dense();
-unsigned long long bounds_fail_distill();
 
 // ---------------------------------------------------------------------------
 // PTX wrappers: mbarrier, TMA, tcgen05

@@ -65,4 +65,8 @@ cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s);
 // expired), read and cleared
 int take_dense_status();
 
+// per source file: the first index out of range of the bounds-check build (0: none)
+unsigned long long bounds_fail_dense();
+unsigned long long bounds_fail_distill();
+
 }  // namespace lq
