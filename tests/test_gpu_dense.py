@@ -414,6 +414,78 @@ def test_other_stream_and_graph():
     lq.lq_check_device()
 
 
+def test_two_streams_at_once():
+    """Calls on two streams with their own workspaces, forward and backward, tiles
+    of CTA pairs among them."""
+    dt = torch.bfloat16
+    sets = [(normal(s, 700, 520, dtype=dt), normal(s + 1, 1200, 520, dtype=dt),
+             normal(s + 2, 1200, 520, dtype=dt), normal(s + 3, 700, 1200, dtype=dt))
+            for s in (0, 10)]
+
+    def step(x, wg, wu, dh, stream=None):
+        h, g, u = lq.lq_gated_linear(x, wg, wu, want_gu=True, stream=stream)
+        return (h,) + lq.lq_gated_linear_bwd(dh, g, u, x, wg, wu, want_db=True, stream=stream)
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(5):
+        for i in (0, 1):
+            got[i].append(step(*sets[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def test_captured_behind_copies_and_joins():
+    """In a captured graph behind a memset, a copy and a join of another stream: the
+    calls wait for all of them."""
+    dt, M, N, K = torch.float16, 260, 392, 1032
+    x, w = normal(1, M, K, dtype=dt), normal(2, N, K, dtype=dt)
+    b, r = normal(3, N, dtype=dt), normal(4, M, N, dtype=dt)
+    want, _ = lq.lq_dense_linear(x, w, b, act=lq.LQ_ACT_SILU, residual=r)
+    xi, wi, ri = torch.zeros_like(x), torch.zeros_like(w), torch.zeros_like(r)
+    y = torch.empty_like(want)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        xi.zero_()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):  # work that takes longer than what runs beside it
+                wi.copy_(w)
+                ri.copy_(r)
+        xi.copy_(x)
+        torch.cuda.current_stream().wait_stream(side)
+        lq.lq_dense_linear(xi, wi, b, act=lq.LQ_ACT_SILU, residual=ri, y=y)
+        lq.lq_dense_linear(xi, wi, b, act=lq.LQ_ACT_SILU, residual=y, y=y)
+        xi.fill_(float("nan"))
+    want2, _ = lq.lq_dense_linear(x, w, b, act=lq.LQ_ACT_SILU, residual=want)
+    for _ in range(5):
+        y.zero_(), wi.zero_(), ri.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want2)
+
+
+def test_same_weight_twice_and_shared_inputs():
+    """The same tensor as both projections, and as several operands of a call."""
+    dt, M, N, K = torch.bfloat16, 150, 72, 72
+    for M in (3, 150):
+        x, w = normal(1, M, K, dtype=dt), normal(2, N, K, scale=0.1, dtype=dt)
+        h, g, u = lq.lq_gated_linear(x, w, w, want_gu=True)
+        h2, _, _ = lq.lq_gated_linear(x, w, w.clone())
+        assert torch.equal(h, h2) and torch.equal(g, u)
+        a = lq.lq_gated_linear_bwd(x, x, x, x, w, w)
+        b = lq.lq_gated_linear_bwd(x.clone(), x.clone(), x.clone(), x, w, w.clone())
+        assert all(torch.equal(p, q) for p, q in zip(a[:3], b[:3]))
+        y, _ = lq.lq_dense_linear(x, w, residual=x)
+        y2, _ = lq.lq_dense_linear(x, w, residual=x.clone())
+        assert torch.equal(y, y2)
+
+
 def test_feed_forward_block_step():
     """One training step of a block's feed-forward half through the entry points:
     gate and up, the down projection with its residual, the output head, the
