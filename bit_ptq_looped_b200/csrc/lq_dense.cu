@@ -524,29 +524,58 @@ __device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, c
 
 // A unit of 16-bit elements of global rows, in two steps: the loads, which may
 // travel while something else is done, and their pieces put into shared memory.
-// What lies outside the matrix is zero.
+// Where rows start anywhere the loads take the aligned vectors around the unit,
+// one more per row (lane l holds that of row l), and are shifted into place in
+// the second step; what they hold beyond the row's end is not stored.
 template <int kRowBytes>
 struct UnitLoad {
   static constexpr int kPieces = kRowBytes / 16;
-  uint4 v[kPieces];
+  uint4 v[kPieces], ext;
+  // the aligned vector at element a; beyond the end of the array zero
+  static __device__ __forceinline__ uint4 vector_at(const uint16_t* src, int64_t a, int64_t total) {
+    if (a + 8 <= total) return *reinterpret_cast<const uint4*>(src + a);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (a + e < total) w[e / 2] |= (uint32_t)src[a + e] << (16 * (e % 2));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
   __device__ __forceinline__ void load(int lane, const uint16_t* src, int64_t ld, int64_t row0,
                                        int64_t col0, int64_t M, int64_t N, bool vec) {
+    const int64_t total = M * ld;
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       const int64_t r = row0 + j * (32 / kPieces) + lane / kPieces;
       const int64_t c = col0 + (lane % kPieces) * 8;
       v[j] = make_uint4(0, 0, 0, 0);
-      if (r >= M || c >= N) continue;
-      // (elements past the row's end are the next row's: they are not stored)
-      v[j] = vec ? *reinterpret_cast<const uint4*>(src + r * ld + c)
-                 : load8_any(src, r * ld + c, M * ld);
+      if (r >= M) continue;
+      if (vec) {
+        if (c < N) v[j] = *reinterpret_cast<const uint4*>(src + r * ld + c);
+      } else {
+        v[j] = vector_at(src, (r * ld + c) & ~(int64_t)7, total);
+      }
     }
+    ext = make_uint4(0, 0, 0, 0);
+    if (!vec && row0 + lane < M)
+      ext = vector_at(src, ((row0 + lane) * ld + col0 + kPieces * 8) & ~(int64_t)7, total);
   }
-  __device__ __forceinline__ void put(unsigned char* stg, int lane) const {
+  __device__ __forceinline__ void put(unsigned char* stg, int lane, int64_t ld, int64_t row0,
+                                      int64_t col0, bool vec) const {
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j)
-      *reinterpret_cast<uint4*>(stg + piece_at<kRowBytes>(j * (32 / kPieces) + lane / kPieces,
-                                                          lane % kPieces)) = v[j];
+    for (int j = 0; j < kPieces; ++j) {
+      const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;
+      uint4 x = v[j];
+      if (!vec) {
+        uint4 y;
+        y.x = __shfl_down_sync(~0u, x.x, 1), y.y = __shfl_down_sync(~0u, x.y, 1);
+        y.z = __shfl_down_sync(~0u, x.z, 1), y.w = __shfl_down_sync(~0u, x.w, 1);
+        const uint32_t e0 = __shfl_sync(~0u, ext.x, row), e1 = __shfl_sync(~0u, ext.y, row),
+                       e2 = __shfl_sync(~0u, ext.z, row), e3 = __shfl_sync(~0u, ext.w, row);
+        if (pc == kPieces - 1) y = make_uint4(e0, e1, e2, e3);
+        x = shift8(x, y, (int)(((row0 + row) * ld + col0) & 7));
+      }
+      *reinterpret_cast<uint4*>(stg + piece_at<kRowBytes>(row, pc)) = x;
+    }
   }
 };
 
@@ -808,7 +837,7 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
           }
         }
         if (kEpi == kEpiDense && P.res) {
-          res.put(stg, lane);
+          res.put(stg, lane, P.ldo, row0, col, P.vec);
           __syncwarp();
           if (u + C::kUnit < C::kCols)
             res.load(lane, P.res, P.ldo, row0, col + C::kUnit, P.M, P.N, P.vec);
@@ -906,7 +935,6 @@ struct RowsParams {
   int M, N, K, act;
 };
 
-constexpr int kRowsWarps = 8;
 constexpr int kRowsUnroll = 4;
 
 // A block owns 16 weight rows (of each factor when gated); its warps take
@@ -916,7 +944,7 @@ constexpr int kRowsUnroll = 4;
 // and calls the first four "k = 2t, 2t+1, 2t+8, 2t+9" of a first MMA, the
 // others of a second; both operands use the same permutation, so the sum is
 // unchanged.  The warps' partial sums are added in shared memory in warp order.
-template <typename T, int kNT, bool kGated>
+template <typename T, int kNT, bool kGated, int kRowsWarps>
 __global__ void __launch_bounds__(32 * kRowsWarps) k_dense_rows(const RowsParams P) {
   constexpr int kF = kGated ? 2 : 1;
   constexpr bool kBf16 = Elem<T>::kFormat == 1;
@@ -1543,14 +1571,17 @@ GemmParams base_params(int64_t M, int64_t N, int64_t kdim) {
   return P;
 }
 
-template <typename T>
-cudaError_t run_rows(const RowsParams& P, bool gated, cudaStream_t s) {
-  const dim3 grid((unsigned)((P.N + 15) / 16)), block(32 * kRowsWarps);
-  if (gated)
-    return P.M <= 8 ? launch_kernel(k_dense_rows<T, 1, true>, grid, block, 0, s, true, P)
-                    : launch_kernel(k_dense_rows<T, 2, true>, grid, block, 0, s, true, P);
-  return P.M <= 8 ? launch_kernel(k_dense_rows<T, 1, false>, grid, block, 0, s, true, P)
-                  : launch_kernel(k_dense_rows<T, 2, false>, grid, block, 0, s, true, P);
+template <typename T, int kNT, bool kGated>
+cudaError_t run_rows(const RowsParams& P, cudaStream_t s) {
+  // Warps that share a block's contraction: 16 where an SM has one block at most and
+  // the contraction gives them work (1 x 2048 x 5632: 5.4 us against 6.9, 16 tokens
+  // 7.6 against 10.8), else 8 (16 x 5632 x 2048: 6.0 against 8.4; 16 x 512 x 512:
+  // 2.2 against 2.7).
+  const int blocks = (P.N + 15) / 16;
+  const dim3 grid((unsigned)blocks);
+  if (blocks <= num_sms() && P.K > 1024)
+    return launch_kernel(k_dense_rows<T, kNT, kGated, 16>, grid, dim3(512), 0, s, true, P);
+  return launch_kernel(k_dense_rows<T, kNT, kGated, 8>, grid, dim3(256), 0, s, true, P);
 }
 
 template <typename T>
@@ -1562,7 +1593,8 @@ cudaError_t forward(const DenseForward& d, cudaStream_t s) {
                  (uint16_t*)d.y,          (uint16_t*)d.aux,         (uint16_t*)d.aux2,
                  (int)d.M,                (int)d.N,                 (int)d.K,
                  d.act};
-    return run_rows<T>(R, gated, s);
+    if (gated) return d.M <= 8 ? run_rows<T, 1, true>(R, s) : run_rows<T, 2, true>(R, s);
+    return d.M <= 8 ? run_rows<T, 1, false>(R, s) : run_rows<T, 2, false>(R, s);
   }
   GemmParams P = base_params(d.M, d.N, d.K);
   P.act = d.act;
