@@ -24,6 +24,9 @@
 // (1.60); in a long series the power cap sets the clock.  One elected lane runs
 // the whole copy or MMA loop: an elected lane inside a loop of the whole warp took
 // 350 clocks per block of a 128 x 64 tile, a plain lane test 540, this form 285.
+// Where a long contraction has few tiles, a cluster of CTAs shares a tile: each takes
+// a part of the contraction, sends its float32 sums to the CTA that finishes the row,
+// and that one adds them in a fixed order.
 //
 // Up to 16 rows (decode) the product is a stream of the weights:
 // k_dense_rows reads each weight once with 16-byte loads and multiplies with
@@ -336,13 +339,25 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t saddr) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(0));
   return r;
 }
+// ... in any CTA of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
 __device__ __forceinline__ void arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
-__device__ __forceinline__ void cluster_sync_all() {
+__device__ __forceinline__ void cluster_arrive() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  cluster_arrive();
+  cluster_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -359,8 +374,10 @@ struct GemmParams {
   int64_t M, N;    // extents of the output (N per factor when gated)
   int64_t ldo;     // elements between output rows
   int n_kb, n_kb1; // contraction blocks; those of the first operand pair
-  int slice_kb;    // blocks of a slice of the contraction (blockIdx.y), n_kb when whole
+  int slice_kb;    // blocks of a slice of the contraction (blockIdx.y, or the cluster's
+                   // member where a cluster shares a tile), n_kb when whole
   int64_t slice_bytes;  // bytes from one slice's output to the next
+  int members;     // CTAs of a cluster that share a tile
   int act;
   int accumulate;
   int vec;         // rows are 16-byte aligned: 16-byte stores
@@ -376,7 +393,11 @@ struct GemmParams {
   uint16_t* aux2;  // the up factor u
 };
 
-template <int kBN, int kPair, int kEpi>
+// Float32 sums of a 64-wide tile that a cluster shares, row by row in shared memory; 16
+// bytes more per row keep the row-per-lane stores free of bank conflicts.
+constexpr int kSumLd = 64 + 4;
+
+template <int kBN, int kPair, int kEpi, bool kShared>
 struct Cfg {
   static constexpr int kEpiWarps = kBN >= 128 ? 8 : 4;
   // columns an epilogue warp handles: its column half of the tile (of each
@@ -387,7 +408,8 @@ struct Cfg {
   // a CTA of a pair holds its own 128 rows of A and its half of B's rows
   static constexpr uint32_t kStageA = BM * BK * 2, kStageB = kBN / kPair * BK * 2;
   static constexpr uint32_t kStageBytes = kStageA + kStageB;
-  static constexpr uint32_t kStaging = kEpiWarps * 32 * 128;
+  // epilogue units, or the sums that a shared tile's members sent
+  static constexpr uint32_t kStaging = kShared ? BM * kSumLd * 4 : kEpiWarps * 32 * 128;
   static constexpr int kStages = (int)((226u * 1024u - 1024u - 512u - kStaging) / kStageBytes);
   static constexpr uint32_t kOffB = kStages * kStageA;
   static constexpr uint32_t kOffStaging = kOffB + kStages * kStageB;
@@ -638,12 +660,136 @@ __device__ __forceinline__ void tile_at(int t, int tm, int tn, int& im, int& in)
   in = r / h;
 }
 
-template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi>
-__global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
+// Eight values of an output row at column c, each rounded once.
+template <typename T>
+__device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t N, bool vec,
+                                       const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = Elem<T>::pack(v[2 * i], v[2 * i + 1]);
+  if (vec) {
+    if (LQ_IN_RANGE(c + 7, N))
+      *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < N) row[c + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+}
+
+// The elements at p[c] .. p[c + 7] that lie below n, zero beyond.
+__device__ __forceinline__ uint4 load8(const uint16_t* p, int64_t c, int64_t n, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4*>(p + c);
+  uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < n) w[e / 2] |= (uint32_t)p[c + e] << (16 * (e % 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T>
+__device__ __forceinline__ void add8(const uint4& w, float (&v)[8]) {
+  const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Elem<T>::unpack(q[i]);
+    v[2 * i] += f.x, v[2 * i + 1] += f.y;
+  }
+}
+
+// The end of a shared tile.  Member m of the cluster finishes the tile's m-th block
+// of BM / members rows: the other members send it their sums of those rows, and it
+// adds the parts in the members' order, eight columns a thread.  Bias and residual
+// are read while the products are under way.
+template <typename T, int kEpi>
+struct SharedTile {
+  static constexpr int kPieces = (kEpi == kEpiGated ? 32 : 64) / 8;
+  static constexpr int kStep = 128 / kPieces;
+  static constexpr int kMax = BM / 2 / kStep;  // pieces of a thread, two members
+  int block;              // rows of a member's block
+  int64_t row_first;      // first row of this member's block
+  int rows;               // rows of the block that exist
+  int64_t col;
+  bool live;
+  uint4 bias, bias2, res[kMax];
+
+  __device__ __forceinline__ void load(const GemmParams& P, int member, int64_t row0,
+                                       int64_t col0) {
+    block = BM / P.members;
+    row_first = row0 + member * block;
+    rows = (int)max((int64_t)0, min((int64_t)block, P.M - row_first));
+    col = col0 + threadIdx.x % kPieces * 8;
+    live = col < P.N;
+    bias = bias2 = make_uint4(0, 0, 0, 0);
+    if (kEpi == kEpiStore || !live) return;
+    if (P.bias) bias = load8(P.bias, col, P.N, P.vec);
+    if (kEpi == kEpiGated && P.bias2) bias2 = load8(P.bias2, col, P.N, P.vec);
+    if (kEpi == kEpiDense && P.res) {
+#pragma unroll
+      for (int i = 0; i < kMax; ++i) {
+        const int r = threadIdx.x / kPieces + i * kStep;
+        if (r < rows) res[i] = load8(P.res + (row_first + r) * P.ldo, col, P.N, P.vec);
+      }
+    }
+  }
+
+  // row `row` of this member's sums, 32 columns from c on, to the row's owner
+  __device__ __forceinline__ void send(uint32_t sums, int member, int row, int c,
+                                       const float (&v)[32]) const {
+    const uint32_t dst = in_cta(
+        sums + ((member * block + row % block) * kSumLd + c) * 4, (uint32_t)(row / block));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(dst + 16 * i),
+                   "f"(v[4 * i]), "f"(v[4 * i + 1]), "f"(v[4 * i + 2]), "f"(v[4 * i + 3])
+                   : "memory");
+  }
+
+  __device__ __forceinline__ void finish(const float* sums, const GemmParams& P) const {
+    if (!live) return;
+#pragma unroll
+    for (int i = 0; i < kMax; ++i) {
+      const int r = threadIdx.x / kPieces + i * kStep;
+      if (r >= rows) break;
+      float v[8] = {}, w[8] = {};
+      for (int m = 0; m < P.members; ++m) {
+        const float4* p = reinterpret_cast<const float4*>(sums + (m * block + r) * kSumLd +
+                                                          threadIdx.x % kPieces * 8);
+        const float4 x = p[0], y = p[1];
+        v[0] += x.x, v[1] += x.y, v[2] += x.z, v[3] += x.w;
+        v[4] += y.x, v[5] += y.y, v[6] += y.z, v[7] += y.w;
+        if (kEpi == kEpiGated) {
+          const float4 g = p[8], h = p[9];
+          w[0] += g.x, w[1] += g.y, w[2] += g.z, w[3] += g.w;
+          w[4] += h.x, w[5] += h.y, w[6] += h.z, w[7] += h.w;
+        }
+      }
+      const int64_t at = (row_first + r) * P.ldo;
+      if (kEpi != kEpiStore) {
+        if (P.bias) add8<T>(bias, v);
+        if (kEpi == kEpiGated && P.bias2) add8<T>(bias2, w);
+        if (P.aux) store8<T>(P.aux + at, col, P.N, P.vec, v);
+        if (kEpi == kEpiGated && P.aux) store8<T>(P.aux2 + at, col, P.N, P.vec, w);
+        apply_act(P.act, v);
+        if (kEpi == kEpiGated) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] *= w[e];
+        } else if (P.res) {
+          add8<T>(res[i], v);
+        }
+      }
+      store8<T>((uint16_t*)P.out + at, col, P.N, P.vec, v);
+    }
+  }
+};
+
+// kShared: the CTAs of a cluster share one tile, each a part of the contraction
+// (gridDim.x: clusters of P.members CTAs, one tile each).
+template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi, bool kShared>
+__global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi, kShared>::kThreads, 1)
     k_dense_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA2,
                  const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmB2,
                  const __grid_constant__ GemmParams P) {
-  using C = Cfg<kBN, kPair, kEpi>;
+  using C = Cfg<kBN, kPair, kEpi, kShared>;
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -661,8 +807,11 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
   const int tm = (int)((P.M + kTileM - 1) / kTileM), tn = (int)((P.N + kTileN - 1) / kTileN);
   const int n_tiles = tm * tn;
   const int rank = kPair == 1 ? 0 : (int)cluster_rank();
-  const int t_first = blockIdx.x / kPair, t_step = gridDim.x / kPair;
-  const int kb_first = blockIdx.y * P.slice_kb, kb_end = min(P.n_kb, kb_first + P.slice_kb);
+  static_assert(!kShared || (kPair == 1 && kBN == 64 && kEpi != kEpiF32), "");
+  const int ctas = kShared ? P.members : kPair;  // CTAs that work on one tile
+  const int member = kShared ? (int)cluster_rank() : 0;
+  const int t_first = blockIdx.x / ctas, t_step = gridDim.x / ctas;
+  const int kb_first = (kShared ? member : (int)blockIdx.y) * P.slice_kb, kb_end = min(P.n_kb, kb_first + P.slice_kb);
 
   pdl_trigger();
   if (threadIdx.x == 0) {
@@ -682,9 +831,11 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (kPair == 2) cluster_sync_all();  // both CTAs' barriers are set up
+  if (kShared) cluster_arrive();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // everything below reads or writes global memory
+  SharedTile<T, kEpi> shared;
 
   if (warp == C::kEpiWarps) {
     // ---- TMA producer: one lane runs the whole loop
@@ -773,6 +924,21 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
       }
       commit_all<kPair>(bar_drain);
       wait_drain(bar_drain, 0u);
+    }
+  } else if (kShared) {
+    // ---- epilogue of a shared tile: send the sums
+    int im, in;
+    tile_at(t_first, tm, tn, im, in);
+    shared.load(P, member, (int64_t)im * kTileM, (int64_t)in * kTileN);
+    const bool ok = __all_sync(~0u, wait_bounded(bar_accf, 0u, abort_flag));
+    cluster_wait();  // every member runs, so that its shared memory may be written
+    if (ok && (int64_t)im * kTileM + 32 * warp < P.M) {
+      tc_fence_after();
+      for (int c = 0; c < kBN; c += 32) {
+        float v[32];
+        load_acc(tmem_base + ((uint32_t)(32 * warp) << 16) + c, v);
+        shared.send(base + C::kOffStaging, member, 32 * warp + lane, c, v);
+      }
     }
   } else {
     // ---- epilogue: warp w reads TMEM lanes 32 (w % 4).. and column part w / 4
@@ -906,6 +1072,13 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi>::kThreads, 1)
   // neither CTA leaves while the other's copies, MMAs or arrivals may still
   // reach its shared memory
   if (kPair == 2) cluster_sync_all();
+  if (kShared) {
+    if (warp >= C::kEpiWarps) cluster_wait();
+    cluster_sync_all();  // all sums have arrived; no member writes another's memory now
+    if (warp < C::kEpiWarps)
+      shared.finish(reinterpret_cast<const float*>(gbase + C::kOffStaging), P);
+    __syncwarp();
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_free<kPair>(tmem_base, C::kTmemCols);
@@ -1469,10 +1642,10 @@ bool operand_map(CUtensorMap* m, const Operand& o, bool mn, bool bf16, int tile_
             : make_map(m, o.p, bf16, o.rows, o.k, o.ld, tile_rows);
 }
 
-template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi>
+template <typename T, int kBN, int kPair, bool kAMn, bool kBMn, int kEpi, bool kShared = false>
 cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, const Operand& b2,
                      const GemmParams& P, int slices, cudaStream_t s) {
-  using C = Cfg<kBN, kPair, kEpi>;
+  using C = Cfg<kBN, kPair, kEpi, kShared>;
   constexpr bool bf16 = Elem<T>::kFormat == 1;
   constexpr int rowsB = kEpi == kEpiGated ? kBN / 2 : kBN / kPair;
   CUtensorMap mA, mA2, mB, mB2;
@@ -1483,7 +1656,7 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
   if ((a2.p != a.p && !operand_map(&mA2, a2, kAMn, bf16, BM)) ||
       (b2.p != b.p && !operand_map(&mB2, b2, kBMn, bf16, rowsB)))
     return cudaErrorInvalidValue;
-  auto* k = k_dense_gemm<T, kBN, kPair, kAMn, kBMn, kEpi>;
+  auto* k = k_dense_gemm<T, kBN, kPair, kAMn, kBMn, kEpi, kShared>;
   static std::atomic<uint64_t> smem_set{0};  // one bit per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1498,7 +1671,9 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   const int64_t slots = std::max(1, num_sms() / kPair / slices);
-  cfg.gridDim = dim3((unsigned)(std::min<int64_t>(tiles, slots) * kPair), (unsigned)slices);
+  const int ctas = kShared ? P.members : kPair;
+  cfg.gridDim = kShared ? dim3((unsigned)(tiles * ctas))
+                        : dim3((unsigned)(std::min<int64_t>(tiles, slots) * kPair), (unsigned)slices);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -1506,10 +1681,10 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kPair;
+  attr[1].val.clusterDim.x = (unsigned)ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = kPair == 1 ? 1 : 2;
+  cfg.numAttrs = ctas == 1 ? 1 : 2;
   return cudaLaunchKernelEx(&cfg, k, mA, mA2, mB, mB2, P);
 }
 
@@ -1526,11 +1701,17 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
 // launch on the host, and the slices' outputs count as well, at 6000 clocks and
 // 2600 bytes a clock.  dw of 8192 x 512 x 512 25 -> 17 us, dx of 64 x 5632 x 2048
 // gated 30 -> 17 us.
+// Where that leaves most SMs idle, a cluster of 2 or 4 CTAs shares a 128 x 64 tile
+// instead and adds its parts up through distributed shared memory; the exchange costs
+// 5000 clocks (256 x 1024 x 1024 would go from 5.4 to 6.2 us).  64 x 2048 x 5632 14.4
+// -> 8.1 us, 128 rows 14.5 -> 9.0, 256 rows 14.6 -> 12.1, gated 14.5 -> 11; 64 x 2048 x
+// 2048 7.4 -> 6.0.  Eight CTAs a tile gain nothing more and do not all fit at once (128
+// of them: 11.5 us against 6.8 with four a tile, 100 x 1003 x 2048).
 struct Shape {
-  int tile, slices;
+  int tile, slices, members;
   int64_t clocks;
 };
-Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices) {
+Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices, bool may_share) {
   const int sms = num_sms();
   struct Kind {
     int tile, bm, bn, slots, per_block, once;
@@ -1539,7 +1720,7 @@ Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices) {
                          {2128, 256, 128, sms / 2, 300, 4300},
                          {128, 128, 128, sms, 330, 3000},
                          {64, 128, 64, sms, 285, 2600}};
-  Shape best{2256, 1, INT64_MAX};
+  Shape best{2256, 1, 1, INT64_MAX};
   for (int slices = 1; slices <= max_slices; slices *= 2) {
     const int kb = (n_kb + slices - 1) / slices;
     if (slices > 1 && (kb < 8 || (int64_t)(slices - 1) * kb >= n_kb)) break;
@@ -1547,8 +1728,15 @@ Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices) {
       const int64_t tiles = ((M + k.bm - 1) / k.bm) * ((N * factors + k.bn - 1) / k.bn) * slices;
       int64_t c = (tiles + k.slots - 1) / k.slots * kb * k.per_block + k.once;
       if (slices > 1) c += 6000 + M * N * 8 * slices / 2600;
-      if (c < best.clocks) best = {k.tile, slices, c};
+      if (c < best.clocks) best = {k.tile, slices, 1, c};
     }
+  }
+  const int64_t tiles = ((M + BM - 1) / BM) * ((N * factors + 63) / 64);
+  for (int members = 2; may_share && members <= 4 && tiles * members <= sms; members *= 2) {
+    const int kb = (n_kb + members - 1) / members;
+    if ((members - 1) * kb >= n_kb) break;  // every member has a part
+    const int64_t c = kb * 285 + 2600 + 5000;
+    if (c < best.clocks) best = {64, 1, members, c};
   }
   return best;
 }
@@ -1556,6 +1744,14 @@ Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices) {
 template <typename T, bool kAMn, bool kBMn, int kEpi>
 cudaError_t run_shape(const Shape& sh, const Operand& a, const Operand& a2, const Operand& b,
                       const Operand& b2, const GemmParams& P, cudaStream_t s) {
+  if constexpr (!kAMn && kEpi != kEpiF32) {
+    if (sh.members > 1) {
+      GemmParams Q = P;
+      Q.members = sh.members;
+      Q.slice_kb = (P.n_kb + sh.members - 1) / sh.members;
+      return run_gemm<T, 64, 1, kAMn, kBMn, kEpi, true>(a, a2, b, b2, Q, 1, s);
+    }
+  }
   switch (sh.tile) {
     case 2256:
       return run_gemm<T, 256, 2, kAMn, kBMn, kEpi>(a, a2, b, b2, P, sh.slices, s);
@@ -1615,10 +1811,10 @@ cudaError_t forward(const DenseForward& d, cudaStream_t s) {
   const Operand x{d.x, d.M, d.K, d.K}, w{d.w, d.N, d.K, d.K};
   if (gated) {
     const Operand w2{d.w2, d.N, d.K, d.K};
-    return run_shape<T, false, false, kEpiGated>(pick_shape(d.M, d.N, P.n_kb, 2, 1), x, x, w, w2, P,
+    return run_shape<T, false, false, kEpiGated>(pick_shape(d.M, d.N, P.n_kb, 2, 1, true), x, x, w, w2, P,
                                                  s);
   }
-  return run_shape<T, false, false, kEpiDense>(pick_shape(d.M, d.N, P.n_kb, 1, 1), x, x, w, w, P,
+  return run_shape<T, false, false, kEpiDense>(pick_shape(d.M, d.N, P.n_kb, 1, 1, true), x, x, w, w, P,
                                                s);
 }
 
@@ -1668,10 +1864,10 @@ bool bwd_by_rows(int64_t M, int64_t N) {
 // shapes of the backward products (half: columns of dz of one factor)
 constexpr int kMaxSlices = 8;
 Shape dx_shape(int64_t M, int64_t half, int64_t K, bool gated) {
-  return pick_shape(M, K, (int)((half + BK - 1) / BK) * (gated ? 2 : 1), 1, kMaxSlices);
+  return pick_shape(M, K, (int)((half + BK - 1) / BK) * (gated ? 2 : 1), 1, kMaxSlices, true);
 }
 Shape dw_shape(int64_t rows, int64_t K, int64_t M) {
-  return pick_shape(rows, K, (int)((M + BK - 1) / BK), 1, kMaxSlices);
+  return pick_shape(rows, K, (int)((M + BK - 1) / BK), 1, kMaxSlices, false);
 }
 
 template <typename T, int kM, bool kGated>

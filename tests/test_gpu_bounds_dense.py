@@ -23,7 +23,7 @@ assert any('liblq_bounds.so' in l for l in open('/proc/self/maps')), 'bounds bui
 r = lambda *s: torch.randn(s, device='cuda').to(torch.bfloat16)
 for M, N, K in ((1, 1, 8), (3, 70, 264), (7, 65, 72), (16, 1000, 264), (17, 64, 64), (129, 257, 200),
                 (300, 1001, 520), (1000, 264, 1024), (2300, 195, 72), (8192, 100, 136),
-                (33, 5632, 264)):
+                (33, 5632, 264), (20, 195, 2048), (129, 1003, 2056), (100, 1040, 264)):
     x, w, w2, b, y, z, u = r(M, K), r(N, K), r(N, K), r(N), r(M, N), r(M, N), r(M, N)
     lq.lq_dense_linear(x, w, b, act=2, residual=y, want_z=True)
     lq.lq_gated_linear(x, w, w2, b, b, want_gu=True)

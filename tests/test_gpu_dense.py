@@ -232,6 +232,93 @@ def test_many_tiles_and_long_contractions():
     check_dense_bwd(70, 5001, 264, torch.bfloat16, lq.LQ_ACT_SILU)
 
 
+# few tiles over a contraction long enough that a cluster of CTAs shares a tile
+SHARED = [(17, 1, 1544), (33, 65, 2048), (40, 72, 1600), (64, 2048, 2048), (100, 1003, 2064),
+          (128, 257, 5632), (129, 2048, 5632), (257, 130, 2056), (300, 264, 8000)]
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,N,K", SHARED)
+def test_shared_tiles(M, N, K, dt):
+    check_dense(M, N, K, TYPES[dt], lq.LQ_ACT_GELU, True, True)
+    check_dense(M, N, K, TYPES[dt], lq.LQ_ACT_NONE, False, False, seed=10)
+    check_gated(M, N, K, TYPES[dt], lq.LQ_ACT_SILU, True, seed=20)
+    check_gated(M, N, K, TYPES[dt], lq.LQ_ACT_RELU, False, seed=30)
+
+
+@pytest.mark.parametrize("dt", TYPES)
+@pytest.mark.parametrize("M,N,K", [(17, 1040, 264), (100, 5001, 72), (129, 2048, 1000),
+                                   (260, 4100, 512)])
+def test_shared_tiles_backward(M, N, K, dt):
+    """dx over N; of the gated form over both factors, whose border lies inside a
+    member's part (N = 1040)."""
+    check_dense_bwd(M, N, K, TYPES[dt], lq.LQ_ACT_SILU)
+    check_dense_bwd(M, N, K, TYPES[dt], lq.LQ_ACT_NONE, seed=10)
+    check_gated_bwd(M, N, K, TYPES[dt], lq.LQ_ACT_GELU)
+
+
+@pytest.mark.parametrize("N", [200, 201, 130, 195])
+def test_shared_tiles_in_place_repeatable_and_within_rows(N):
+    dt, K = torch.bfloat16, 2048
+    for M in (20, 130):
+        x, w = normal(1, M, K, dtype=dt), normal(2, N, K, scale=K ** -0.5, dtype=dt)
+        r = normal(3, M, N, dtype=dt)
+        want, _ = lq.lq_dense_linear(x, w, residual=r)
+        assert torch.equal(want, lq.lq_dense_linear(x, w, residual=r)[0])
+        buf = torch.full((M * N + 4096,), 7.0, dtype=dt, device="cuda")
+        y = buf[:M * N].view(M, N)
+        y.copy_(r)
+        lq.lq_dense_linear(x, w, residual=y, y=y)
+        assert torch.equal(y, want) and bool((buf[M * N:] == 7).all())
+        # a row's values do not depend on the rows beside it
+        bad = x.clone()
+        bad[3] = float("nan")
+        got = lq.lq_dense_linear(bad, w, residual=r)[0]
+        keep = torch.arange(M, device="cuda") != 3
+        assert torch.equal(got[keep], want[keep]) and bool(got[3].isnan().all())
+
+
+def test_shared_tiles_on_two_streams_and_replayed():
+    """Chains of calls that read each other's outputs, on two streams at once and as
+    a replayed graph, against the same chain alone."""
+    dt, n = torch.bfloat16, 2048
+    ws = [normal(i, n, n, scale=n ** -0.5, dtype=dt) for i in range(3)]
+
+    def chain(x, outs):
+        for i, y in enumerate(outs):
+            lq.lq_dense_linear(x, ws[i % 3], act=lq.LQ_ACT_SILU, residual=x, y=y)
+            x = y
+
+    xs = [normal(10 + i, 60 + i, n, dtype=dt) for i in range(2)]
+    outs = [[torch.empty_like(x) for _ in range(12)] for x in xs]
+    want = []
+    for x, o in zip(xs, outs):
+        chain(x, o)
+        torch.cuda.synchronize()
+        want.append([y.clone() for y in o])
+        for y in o:
+            y.zero_()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for st, x, o in zip(streams, xs, outs):
+            with torch.cuda.stream(st):
+                chain(x, o)
+    torch.cuda.synchronize()
+    for o, e in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, e))
+    for y in outs[0]:
+        y.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain(xs[0], outs[0])
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs[0], want[0]))
+    lq.lq_check_device()
+
+
 @pytest.mark.parametrize("N", [200, 201, 130, 195])
 def test_residual_in_place_and_repeatable(N):
     dt = torch.bfloat16
