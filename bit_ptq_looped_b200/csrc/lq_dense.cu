@@ -1699,14 +1699,15 @@ cudaError_t run_gemm(const Operand& a, const Operand& a2, const Operand& b, cons
 // A long contraction over few tiles is cut into slices (only where the caller has
 // room for their float32 outputs, which another pass adds up): that pass, with its
 // launch on the host, and the slices' outputs count as well, at 6000 clocks and
-// 2600 bytes a clock.  dw of 8192 x 512 x 512 25 -> 17 us, dx of 64 x 5632 x 2048
-// gated 30 -> 17 us.
+// 2600 bytes a clock.  dw of 8192 x 512 x 512 25 -> 17 us.
 // Where that leaves most SMs idle, a cluster of 2 or 4 CTAs shares a 128 x 64 tile
 // instead and adds its parts up through distributed shared memory; the exchange costs
 // 5000 clocks (256 x 1024 x 1024 would go from 5.4 to 6.2 us).  64 x 2048 x 5632 14.4
 // -> 8.1 us, 128 rows 14.5 -> 9.0, 256 rows 14.6 -> 12.1, gated 14.5 -> 11; 64 x 2048 x
-// 2048 7.4 -> 6.0.  Eight CTAs a tile gain nothing more and do not all fit at once (128
-// of them: 11.5 us against 6.8 with four a tile, 100 x 1003 x 2048).
+// 2048 7.4 -> 6.0; dx of 64 x 5632 x 2048 14.1 -> 7.8, of 128 x 49152 x 2048 112 -> 39.
+// 128 x 128 tiles shared in the same way take as long.  Eight CTAs a tile gain nothing
+// more and do not all fit at once (128 of them: 11.5 us against 6.8 with four a tile,
+// 100 x 1003 x 2048).
 struct Shape {
   int tile, slices, members;
   int64_t clocks;
