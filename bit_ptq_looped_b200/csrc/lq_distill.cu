@@ -10,9 +10,13 @@
 //   dz_j = w / T (C q_j - p_j)                 j listed, C = sum p + R
 //   dz_j = w / T  q_j (C - R S / S_rest)       otherwise,
 // S the sum of exp(z / T) over the vocabulary and S_rest that over the entries
-// that are not listed, Q_rest = S_rest / S.  S_rest is summed directly (not as
-// a difference, which loses everything when the listed entries hold nearly
-// all of the student's mass).
+// that are not listed, Q_rest = S_rest / S.  With a rest class S_rest is summed
+// directly (not as a difference, which loses everything when the listed entries hold
+// nearly all of the student's mass) and relative to the largest logit that is not
+// listed, m_rest: it keeps its digits however far those logits lie below the listed
+// ones.  S is put together from it and the listed entries' sum in float64, log Q_rest
+// from logarithms, and with f = w / T (C exp((m_rest - m) / T) / S - R / S_rest) an
+// entry that is not listed gets f exp((z_j - m_rest) / T): no factor overflows.
 //
 // What bounds it is memory, each logit read once and each gradient written
 // once, and next to it the exponential unit (two exponentials per logit, 16 per
@@ -46,6 +50,18 @@ constexpr int kMaxSmem = 164 * 1024;  // 64 KB of bitmap, 96 KB of listed entrie
 constexpr int kMaxCluster = 8;
 constexpr float kNegInf = -INFINITY;
 
+// eight 16-bit elements, kInf where bit i of marks is set
+template <uint32_t kInf>
+__device__ __forceinline__ uint4 hide16(const uint4& w, uint32_t marks) {
+  uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((marks >> (2 * i)) & 1u) q[i] = (q[i] & 0xFFFF0000u) | kInf;
+    if ((marks >> (2 * i)) & 2u) q[i] = (q[i] & 0x0000FFFFu) | (kInf << 16);
+  }
+  return make_uint4(q[0], q[1], q[2], q[3]);
+}
+
 template <typename T>
 struct Log;  // element access of a logit type
 template <>
@@ -63,6 +79,11 @@ struct Log<float> {
   }
   static __device__ __forceinline__ uint4 nothing() {  // -inf throughout
     return make_uint4(0xFF800000u, 0xFF800000u, 0xFF800000u, 0xFF800000u);
+  }
+  // -inf where bit i of marks is set
+  static __device__ __forceinline__ uint4 hide(const uint4& w, uint32_t marks) {
+    return make_uint4((marks & 1u) ? 0xFF800000u : w.x, (marks & 2u) ? 0xFF800000u : w.y,
+                      (marks & 4u) ? 0xFF800000u : w.z, (marks & 8u) ? 0xFF800000u : w.w);
   }
   // running maximum of 16-byte vectors, in the type's own pairs
   using Run = float;
@@ -97,6 +118,9 @@ struct Log<__nv_bfloat16> {
   }
   static __device__ __forceinline__ uint4 nothing() {
     return make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);
+  }
+  static __device__ __forceinline__ uint4 hide(const uint4& w, uint32_t marks) {
+    return hide16<0xFF80u>(w, marks);
   }
   using Run = __nv_bfloat162;
   static __device__ __forceinline__ Run run_start() { return __float2bfloat162_rn(kNegInf); }
@@ -133,6 +157,9 @@ struct Log<__half> {
   }
   static __device__ __forceinline__ uint4 nothing() {
     return make_uint4(0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u, 0xFC00FC00u);
+  }
+  static __device__ __forceinline__ uint4 hide(const uint4& w, uint32_t marks) {
+    return hide16<0xFC00u>(w, marks);
   }
   using Run = __half2;
   static __device__ __forceinline__ Run run_start() { return __float2half2_rn(kNegInf); }
@@ -192,17 +219,18 @@ __device__ __forceinline__ T warp_sum(T v) {
 
 // what a slice tells the others
 struct Part {
-  float m, m2nd;     // maximum of its logits; of its teacher entries (rest class: listed logits)
-  double s, s2nd;    // the sums of exponentials that go with them (rest class: s over
-                     // those not listed)
+  float m, m2nd;     // maximum of its logits (rest class: of those not listed); of its
+                     // teacher entries (rest class: of the listed logits)
+  double s, s2nd;    // the sums of exponentials that go with them
   double p_sum;      // rest class: sum of p
 };
 // a row's numbers, worked out by one thread.  What the gradient waits for needs
 // divisions only; the logarithms come at the end, for the loss alone.
 struct RowNumbers {
-  float m2;      // exponents are z c2 - m2
+  float m2;      // exponents of listed entries are z c2 - m2
+  float r2;      // of entries that are not listed z c2 - r2
   float f_rest;  // gradient of an entry that is not listed, over its exponential
-  float f_top;   // C / S times the scale, the same for listed entries
+  float f_top;   // C / S times the scale: what q adds to a listed entry's
   float inv_ts;  // no rest class: one over the listed exponentials' sum, 0 if there is none
   float tm2;     // exponents of p are t c2 - tm2 (no rest class)
 };
@@ -410,6 +438,13 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   for (int b = 0; b < n_batch; ++b) {
     uint4 y[kUnroll];
     if (b + 1 < n_batch) batch(y, b + 1);
+    if (kTail) {  // listed entries do not count here
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int e = min(sl.v_lo + tid + (b * kUnroll + u) * kThreads, sl.v_hi - 1) * kE;
+        x[u] = Log<T>::hide(x[u], bits[e >> 5] >> (e & 31));
+      }
+    }
     typename Log<T>::Run run = Log<T>::run_start();
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) run = Log<T>::run_max(run, x[u]);
@@ -419,13 +454,6 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     for (int u = 0; u < kUnroll; ++u) {
       float f[kE];
       Log<T>::unpack(x[u], f);
-      if (kTail) {
-        const int e = min(sl.v_lo + tid + (b * kUnroll + u) * kThreads, sl.v_hi - 1) * kE;
-        const uint32_t marks = bits[e >> 5] >> (e & 31);
-#pragma unroll
-        for (int i = 0; i < kE; ++i)
-          if ((marks >> i) & 1u) f[i] = kNegInf;
-      }
 #pragma unroll
       for (int i = 0; i < kE; i += 2) {
         const float2 q = ffma2(make_float2(f[i], f[i + 1]), c2v, nm2);
@@ -438,8 +466,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   float z_edge = 0.f;
   if (tid < sl.n_edge) {
     z_edge = Log<T>::get(zs + sl.edge(tid));
-    raise(z_edge);
-    if (!kTail || !marked(sl.edge(tid))) s2.x += ex2(fmaf(z_edge, P.c2, -r1.m2));
+    if (!kTail || !marked(sl.edge(tid))) {
+      raise(z_edge);
+      s2.x += ex2(fmaf(z_edge, P.c2, -r1.m2));
+    }
   }
   if (gs) batch(x, 0);  // the second pass's first batch
   r1.s = s2.x + s2.y;
@@ -491,15 +521,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 
   // the row's numbers, from the slices in order
   double S = 0.0, total = 0.0, TS = 0.0, R = 0.0;
+  double to_top = 0.0;  // rest class: its largest exponent below the row's
   if (tid == 0) {
     float M = kNegInf, M2nd = kNegInf;
     for (int r = 0; r < n_parts; ++r) {
       M = fmaxf(M, parts[r].m);
       M2nd = fmaxf(M2nd, parts[r].m2nd);
     }
-    // exponents of listed logits are never above the row's own maximum
     const float M2 = M == kNegInf ? 0.f : __fmul_rn(M, P.c2);
-    const float N2 = kTail ? M2 : M2nd == kNegInf ? 0.f : __fmul_rn(M2nd, P.c2);
+    const float N2 = M2nd == kNegInf ? 0.f : __fmul_rn(M2nd, P.c2);
     auto scaled = [&](float m, double v, float to2) {
       if (m == kNegInf) return 0.0;
       const float d = __fmul_rn(m, P.c2) - to2;
@@ -511,18 +541,30 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       second += scaled(parts[r].m2nd, parts[r].s2nd, N2);
       TS += parts[r].p_sum;
     }
-    total = kTail ? S + second : S;
-    TS = kTail ? TS : second;
-    R = kTail && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
-    const double C = kTail ? TS + R : (TS > 0.0 ? 1.0 : 0.0);
-    if (!(S > 0.0)) R = 0.0;  // nothing outside the list: no rest class
-    const float scale_t = w * P.inv_temp / (float)total;
     RowNumbers n;
-    n.m2 = M2;
-    n.f_rest = scale_t * (float)(R > 0.0 ? C - R * total / S : C);
-    n.f_top = scale_t * (float)C;
-    n.inv_ts = !kTail && TS > 0.0 ? 1.f / (float)TS : 0.f;
-    n.tm2 = N2;
+    if (kTail) {
+      // both sums in units of the larger maximum
+      const float top2 = M2nd == kNegInf || M > M2nd ? M2 : N2;
+      to_top = (double)M2 - (double)top2;
+      const float up = to_top == 0.0 ? 1.f : exp2f((float)to_top);
+      total = (M == kNegInf ? S : S * (double)up) + scaled(M2nd, second, top2);
+      R = 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
+      const double C = TS + R;
+      if (!(S > 0.0)) R = 0.0;  // nothing outside the list: no rest class
+      const float scale = w * P.inv_temp, f = (float)C / (float)total;
+      n.m2 = top2;
+      n.r2 = M2;
+      n.f_rest = S > 0.0 ? scale * (f * up - (float)R / (float)S) : 0.f;
+      n.f_top = scale * f;
+      n.inv_ts = n.tm2 = 0.f;
+    } else {
+      total = S;
+      TS = second;
+      n.m2 = n.r2 = M2;
+      n.f_rest = n.f_top = TS > 0.0 ? w * P.inv_temp / (float)total : 0.f;
+      n.inv_ts = TS > 0.0 ? 1.f / (float)TS : 0.f;
+      n.tm2 = N2;
+    }
     row_n = n;
   }
   __syncthreads();
@@ -536,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 
   // second pass: the gradient of entries that are not listed
   if (gs) {
-    const float2 fr = make_float2(n.f_rest, n.f_rest), nn = make_float2(-n.m2, -n.m2);
+    const float2 fr = make_float2(n.f_rest, n.f_rest), nn = make_float2(-n.r2, -n.r2);
     uint4* out = reinterpret_cast<uint4*>(gs) + sl.v_lo + tid;
     auto grad = [&](const uint4& x) {
       float f[kE];
@@ -570,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       for (int u = 0; u < kUnroll; ++u) x[u] = y[u];
     }
     if (tid < sl.n_edge)
-      Log<T>::put(gs + sl.edge(tid), n.f_rest * ex2(fmaf(z_edge, P.c2, -n.m2)));
+      Log<T>::put(gs + sl.edge(tid), n.f_rest * ex2(fmaf(z_edge, P.c2, -n.r2)));
     __syncthreads();
   }
   // The listed entries: their gradients over it, and the loss up to the
@@ -614,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     double l = 0.0;
     for (int r = 0; r < n_parts; ++r) l += loss_parts[r];
     l *= 0.6931471805599453;
-    if (kTail && R > 0.0) l += R * (log(R) - log(S / total));
+    if (kTail && R > 0.0)
+      l += R * (log(R * total / S) - to_top * 0.6931471805599453);
     P.loss[row] = (float)((double)w * l);
   }
 }

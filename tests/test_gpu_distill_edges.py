@@ -1,0 +1,154 @@
+"""lq_distill_loss where its numbers are far apart: listed logits far above the
+others.  The oracle differentiates the float64 loss itself.
+
+Tolerances, derived before the first run.  With d = (reference maximum - z) /
+temp >= 0 an exponential carries 3 * 2^-24 d from its exponent (difference,
+factor, product), 2^-22 from the hardware, and a float32 sum of a thread some
+hundred roundings of 2^-24 at random: e(d) = 2^-18 + 2^-22 d relative for an
+exponential over its sum.  d averaged over a softmax of V entries is at most
+log V < 12, so a logarithm of a sum is off by 2^-18.  log q and log Q add the
+rounding of log2(e) / temp, 2^-24 of their size: 2^-18 + 2^-23 |log q|.  The
+teacher's p carries 2^-22 + 2^-23 |log p|, and R = 1 - sum p the same of the sum:
+d_R = 2^-20 for p over a few hundred entries (sum p |log p| <= log k < 6).
+"""
+import math
+
+import pytest
+import torch
+
+from bit_ptq_looped_b200 import lq
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+# the smallest step near zero (the exponential flushes float32 subnormals)
+SUB = {torch.float32: 2.0 ** -124, torch.bfloat16: 2.0 ** -124, torch.float16: 2.0 ** -24}
+D_R = 2.0 ** -20
+
+
+def rand(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda") * scale
+
+
+def row_oracle(z, tv, ti, t_lse, w, temp):
+    """One row: (loss, grad, tolerance of each but for the last rounding)."""
+    V = z.numel()
+    Z = z.double().cpu().requires_grad_()
+    y = Z / temp
+    pos, val = [], []
+    for v, t in zip(ti.tolist(), tv.double().tolist()):
+        if 0 <= v < V and v not in pos:
+            pos.append(v), val.append(t / temp)
+    zero = torch.zeros(V, dtype=torch.float64)
+    if w == 0 or (t_lse is None and not pos):
+        return 0.0, zero, 0.0, zero
+    idx = torch.tensor(pos, dtype=torch.int64)
+    hidden = torch.zeros(V, dtype=torch.bool)
+    hidden[idx] = True
+    t = torch.tensor(val, dtype=torch.float64)
+    R = 0.0
+    if t_lse is None:
+        log_p = torch.log_softmax(t, 0)
+    else:
+        log_p = t - t_lse
+        R = max(0.0, 1.0 - float(log_p.exp().sum()))
+    p = log_p.exp()
+    lse = torch.logsumexp(y, 0)
+    on = p > 0
+    log_q = y[idx][on] - lse
+    loss = (p[on] * (log_p[on] - log_q)).sum()
+    rest = y[~hidden]
+    log_Q = torch.tensor(0.0)
+    if R > 0 and bool((rest > -math.inf).any()):
+        lse_rest = torch.logsumexp(rest, 0)
+        log_Q = lse_rest - lse
+        loss = loss + R * (math.log(R) - log_Q)
+    else:
+        R = 0.0
+    g, = torch.autograd.grad(loss, Z)
+    with torch.no_grad():
+        tl = float((p[on] * (2.0 ** -18 + 2.0 ** -23 * log_q.abs() + 2.0 ** -22 +
+                             2.0 ** -23 * log_p[on].abs())).sum())
+        # an error of p moves its own term as well
+        tl += float((p[on] * (2.0 ** -22 + 2.0 ** -23 * log_p[on].abs()) *
+                     (log_p[on] - log_q).abs()).sum())
+        C = float(p.sum()) + R
+        q = (y - lse).exp()
+        tg = C * q * (2.0 ** -18 + 2.0 ** -22 * (y.max() - y).clamp(max=1e4))
+        tg[idx] += p * (2.0 ** -21 + 2.0 ** -22 * log_p.clamp(min=-1e4).abs())
+        if R:
+            size = abs(math.log(R)) + abs(float(log_Q))
+            tl += R * (2.0 ** -18 + 2.0 ** -23 * size) + D_R * (2 + size)
+            s = torch.where(hidden, zero, (y - lse_rest).exp())
+            tg += s * (R * (2.0 ** -18 + 2.0 ** -22 * (rest.max() - y).clamp(0, 1e4)) + D_R)
+    return w * float(loss.detach()), g * w, abs(w) * tl, abs(w) / temp * tg
+
+
+def check(z, tv, ti, t_lse=None, w=None, temp=1.0, rows=None):
+    """The whole call against the oracle on some of its rows."""
+    loss, grad = lq.lq_distill_loss(z, tv, ti, t_lse=t_lse, weight=w, temp=temp, want_grad=True)
+    only, _ = lq.lq_distill_loss(z, tv, ti, t_lse=t_lse, weight=w, temp=temp)
+    assert torch.equal(only.nan_to_num(), loss.nan_to_num()), "the gradient changes the loss"
+    eps = torch.finfo(z.dtype).eps / 2
+    for m in range(z.shape[0]) if rows is None else rows:
+        L, G, tl, tg = row_oracle(z[m], tv[m], ti[m], None if t_lse is None else float(t_lse[m]),
+                                  1.0 if w is None else float(w[m]), temp)
+        got = float(loss[m])
+        assert abs(got - L) <= tl + 2.0 ** -24 * abs(L), (m, got, L, tl)
+        g = grad[m].double().cpu()
+        err = (g - G).abs() / (tg + eps * (G.abs() + tg) + SUB[z.dtype])
+        assert bool((err <= 1).all()), (m, int((~(err <= 1)).sum()), float(err.max()),
+                                        int(err.nan_to_num(math.inf).argmax()))
+    return loss, grad
+
+
+def apart(seed, M, V, k, dt, gap, R):
+    """k listed logits about `gap` above the others; the teacher leaves mass R."""
+    ti = torch.stack([torch.randperm(V, generator=torch.Generator().manual_seed(seed + m))[:k]
+                      for m in range(M)]).cuda()
+    z = rand(seed, M, V)
+    z.scatter_add_(1, ti, torch.full((M, k), float(gap), device="cuda"))
+    tv = rand(seed + 1, M, k)
+    return z.to(dt), tv, ti, torch.logsumexp(tv.double(), 1) - math.log(1 - R)
+
+
+# a row in one CTA, and one shared by a cluster of eight
+@pytest.mark.parametrize("M,V,k", [(3, 1000, 64), (2, 49152, 64)])
+@pytest.mark.parametrize("gap", [-110, 60, 80, 84, 86, 90, 110, 200, 800, 10000])
+@pytest.mark.parametrize("temp", [0.5, 1.0])
+def test_rest_class_far_below_the_list(M, V, k, gap, temp):
+    for name, R in (("f32", 0.1), ("bf16", 0.95), ("f16", 0.5)):
+        z, tv, ti, lse = apart(gap + V, M, V, k, TYPES[name], gap, R)
+        lse = torch.logsumexp(tv.double() / temp, 1) - math.log(1 - R)
+        loss, grad = check(z, tv, ti, t_lse=lse.float(), temp=temp)
+        if gap > 200:  # the unlisted entries' gradients sum to -R / temp
+            sums = grad.double().scatter(1, ti, 0.0).sum(1) * temp
+            assert float((sums + R).abs().max()) <= 2.0 ** -8 * R + 1e-3
+
+
+def test_one_listed_logit_far_above_the_others():
+    z = torch.zeros(4, 49152, device="cuda")
+    z[:, 17] = 110.0
+    tv, ti = torch.zeros(4, 1, device="cuda"), torch.full((4, 1), 17, device="cuda")
+    check(z, tv, ti, t_lse=torch.full((4,), -math.log(0.9), device="cuda"))
+
+
+@pytest.mark.parametrize("mask", [-100.0, -700.0, -1e4])
+def test_a_finite_mask_over_everything_unlisted(mask):
+    for name in ("f32", "bf16"):
+        z, tv, ti, lse = apart(5, 2, 20011, 100, TYPES[name], 0.0, 0.3)
+        rest = torch.full_like(z, mask).scatter(1, ti, z.gather(1, ti))
+        check(rest, tv, ti, t_lse=lse.float())
+
+
+def test_a_row_does_not_depend_on_the_batch():
+    """One CTA a row (a batch of 400) and eight (the row alone): the same loss and
+    gradient within twice the tolerance."""
+    for gap in (0, 86, 110, 800):
+        z, tv, ti, lse = apart(gap, 400, 20011, 50, torch.float32, gap, 0.4)
+        loss, grad = check(z, tv, ti, t_lse=lse.float(), rows=(0, 399))
+        one, g1 = check(z[399:].clone(), tv[399:].clone(), ti[399:].clone(),
+                        t_lse=lse[399:].float())
+        assert float((one - loss[399:]).abs()) <= 2.0 ** -17 * (1 + float(loss[399].abs()))
+        assert float((g1[0] - grad[399]).abs().max()) <= 2.0 ** -17
