@@ -5,7 +5,8 @@
 // indices v_i.  With temperature T, q = softmax(z / T) and
 //   no rest class:  p = softmax(t / T) over the listed entries, R = 0;
 //   rest class:     p_i = exp(t_i / T - L) with the teacher's log-partition L,
-//                   R = max(0, 1 - sum p) for everything that is not listed;
+//                   R = max(0, 1 - sum p) for everything that is not listed (0
+//                   where the student has no mass there, Q_rest = 0);
 //   loss = w (sum_i p_i (log p_i - log q_{v_i}) + R (log R - log Q_rest)),
 //   dz_j = w / T (C q_j - p_j)                 j listed, C = sum p + R
 //   dz_j = w / T  q_j (C - R S / S_rest)       otherwise,
@@ -548,9 +549,9 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       to_top = (double)M2 - (double)top2;
       const float up = to_top == 0.0 ? 1.f : exp2f((float)to_top);
       total = (M == kNegInf ? S : S * (double)up) + scaled(M2nd, second, top2);
-      R = 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
+      // nothing outside the list: no rest class, neither in the loss nor in its gradient
+      R = S > 0.0 && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
       const double C = TS + R;
-      if (!(S > 0.0)) R = 0.0;  // nothing outside the list: no rest class
       const float scale = w * P.inv_temp, f = (float)C / (float)total;
       n.m2 = top2;
       n.r2 = M2;

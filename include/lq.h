@@ -429,8 +429,9 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *       not listed is one more class with mass R = max(0, 1 - sum p):
  *   loss[m] = w[m] (sum_i p_i (log p_i - log q_{v_i}) + R (log R - log Q)),
  *       Q the student's mass outside the list (the R term is left out where R
- *       or Q is zero);
- *   grad    = d loss[m] / d z.
+ *       is zero, or Q is because every logit outside the list is -inf);
+ *   grad    = d loss[m] / d z, of the loss as returned: where the R term is left
+ *       out of the loss it is left out of the gradient.
  *   d_logits    M x V, dtype LQ_F32, LQ_BF16 or LQ_F16; entries may be -inf
  *               (masked vocabulary), not all of a row.  Rows start anywhere: V is
  *               arbitrary.

@@ -1,5 +1,5 @@
 """lq_distill_loss where its numbers are far apart: listed logits far above the
-others.  The oracle differentiates the float64 loss itself.
+others, nothing outside the list.  The oracle differentiates the float64 loss itself.
 
 Tolerances, derived before the first run.  With d = (reference maximum - z) /
 temp >= 0 an exponential carries 3 * 2^-24 d from its exponent (difference,
@@ -152,3 +152,53 @@ def test_a_row_does_not_depend_on_the_batch():
                         t_lse=lse[399:].float())
         assert float((one - loss[399:]).abs()) <= 2.0 ** -17 * (1 + float(loss[399].abs()))
         assert float((g1[0] - grad[399]).abs().max()) <= 2.0 ** -17
+
+
+def test_no_mass_outside_the_list():
+    """Every unlisted logit -inf, or nothing unlisted at all, while the teacher leaves
+    mass R: the returned loss has no R term, and its gradient P q - p sums to zero."""
+    for M, V, k in ((3, 900, 11), (2, 33001, 50), (4, 17, 17)):
+        for name, R in (("f32", 0.3), ("bf16", 0.9), ("f16", 0.01)):
+            z, tv, ti, lse = apart(V, M, V, k, TYPES[name], 0.0, R)
+            only = torch.full_like(z, -math.inf).scatter(1, ti, z.gather(1, ti))
+            loss, grad = check(only, tv, ti, t_lse=lse.float())
+            assert not grad.gather(1, ti).isnan().any()
+            assert not grad.scatter(1, ti, 0.0).any()
+            eps = torch.finfo(z.dtype).eps / 2
+            size = grad.double().abs().sum(1)
+            assert bool((grad.double().sum(1).abs() <= 2.0 ** -17 + eps * size + k * SUB[z.dtype])
+                        .all())
+
+
+def test_gradient_against_differences_without_mass_outside():
+    """Central differences over the listed logits of such a row; noise and cubic term
+    as for ordinary rows: the loss is known to 2^-20 of its logarithms (below 8)."""
+    z, tv, ti, lse = apart(3, 3, 120, 9, torch.float32, 0.0, 0.4)
+    z = torch.full_like(z, -math.inf).scatter(1, ti, z.gather(1, ti))
+    lse = lse.float()
+    _, grad = lq.lq_distill_loss(z, tv, ti, t_lse=lse, want_grad=True)
+    step = 2.0 ** -4
+    for trial in range(4):
+        d = torch.sign(rand(40 + trial, 3, 120))
+        up = lq.lq_distill_loss(z + step * d, tv, ti, t_lse=lse)[0]
+        dn = lq.lq_distill_loss(z - step * d, tv, ti, t_lse=lse)[0]
+        num = (up - dn).double() / (2 * step)
+        ana = (grad.double() * d.double()).sum(1)
+        assert bool(((num - ana).abs() <= 2.0 ** -17 / (2 * step) + step ** 2).all())
+
+
+@pytest.mark.parametrize("name", TYPES)
+def test_masked_entries_next_to_ordinary_ones(name):
+    """-inf and the type's lowest value between ordinary logits, listed or not."""
+    dt = TYPES[name]
+    teacher = rand(6, 4, 900, scale=3.0)
+    z = (teacher + rand(7, 4, 900, scale=0.7)).to(dt)
+    tv, ti = torch.topk(teacher, 11, dim=1)
+    hide = torch.ones(900, dtype=torch.bool, device="cuda")
+    hide[ti.flatten()] = False
+    at = hide.nonzero().flatten()
+    z[:, at[::3]] = -math.inf
+    z[:, at[1::3]] = torch.finfo(dt).min
+    for lse in (None, torch.logsumexp(teacher, 1)):
+        loss, grad = check(z, tv, ti, t_lse=lse)
+        assert not grad[z == -math.inf].any()
