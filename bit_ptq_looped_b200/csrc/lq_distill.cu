@@ -228,25 +228,31 @@ struct Part {
 // a row's numbers, worked out by one thread.  What the gradient waits for needs
 // divisions only; the logarithms come at the end, for the loss alone.
 struct RowNumbers {
-  float m2;      // exponents of listed entries are z c2 - m2
-  float r2;      // of entries that are not listed z c2 - r2
+  float m;       // exponents of listed entries are (z - m) c2
+  float m_rest;  // of entries that are not listed (z - m_rest) c2
   float f_rest;  // gradient of an entry that is not listed, over its exponential
   float f_top;   // C / S times the scale: what q adds to a listed entry's
   float inv_ts;  // no rest class: one over the listed exponentials' sum, 0 if there is none
-  float tm2;     // exponents of p are t c2 - tm2 (no rest class)
+  float tm;      // exponents of p are (t - tm) c2 (no rest class)
 };
 
-// Running maximum and sum of exponentials: s counts in units of 2^m2, m2 = m c2
-// rounded (never contracted into a multiply-add, or two sums with the same
-// maximum would count in different units).
+// Running maximum and sum of exponentials.  An exponent is the difference of a logit
+// and the maximum, times c2: z c2 - m c2 would be one multiply-add, but both products
+// leave float32's range where logits are masked with their type's lowest value or the
+// temperature is small, and inf - inf is no number.  The difference may at worst be
+// -inf, which counts nothing.  ref: the maximum, 0 while there is none.
 struct Run1 {
-  float m, m2, s;
+  float m, s;
 };
-// the two as one, in a fixed order of lanes
+__device__ __forceinline__ float ref(float m) { return m == kNegInf ? 0.f : m; }
+__device__ __forceinline__ float ex2_from(float z, float from, float c2) {
+  return ex2((z - from) * c2);
+}
+// the lanes' as one, in a fixed order
 __device__ __forceinline__ Run1 warp_join(Run1 r, float c2) {
-  const float m = warp_max(r.m), m2 = m == kNegInf ? 0.f : __fmul_rn(m, c2);
-  const float s = warp_sum(r.m == kNegInf ? 0.f : r.s * ex2(r.m2 - m2));
-  return {m, m2, s};
+  const float m = warp_max(r.m);
+  const float s = warp_sum(r.m == kNegInf ? 0.f : r.s * ex2_from(r.m, m, c2));
+  return {m, s};
 }
 
 // log2 p of a listed entry, in float64: logit and log-partition may be far larger
@@ -422,17 +428,16 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   };
   auto marked = [&](int e) { return (bits[e >> 5] >> (e & 31)) & 1u; };
 
-  // First pass: running maximum and sum; base-2 exponents are z c2 - m2.  A
-  // batch first raises the maximum (packed), then adds its exponentials.
-  Run1 r1 = {kNegInf, 0.f, 0.f};
+  // First pass: running maximum and sum.  A batch first raises the maximum
+  // (packed), then adds its exponentials.
+  Run1 r1 = {kNegInf, 0.f};
   float2 s2 = make_float2(0.f, 0.f);
   const float2 c2v = make_float2(P.c2, P.c2);
   auto raise = [&](float to) {
     if (to > r1.m) {
-      const float n2 = __fmul_rn(to, P.c2), f = r1.m == kNegInf ? 0.f : ex2(r1.m2 - n2);
+      const float f = ex2_from(r1.m, to, P.c2);
       s2 = fmul2(s2, make_float2(f, f));
       r1.m = to;
-      r1.m2 = n2;
     }
   };
 
@@ -450,14 +455,14 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) run = Log<T>::run_max(run, x[u]);
     raise(Log<T>::run_end(run));
-    const float2 nm2 = make_float2(-r1.m2, -r1.m2);
+    const float2 nm = make_float2(-ref(r1.m), -ref(r1.m));
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       float f[kE];
       Log<T>::unpack(x[u], f);
 #pragma unroll
       for (int i = 0; i < kE; i += 2) {
-        const float2 q = ffma2(make_float2(f[i], f[i + 1]), c2v, nm2);
+        const float2 q = fmul2(fadd2(make_float2(f[i], f[i + 1]), nm), c2v);
         s2 = fadd2(s2, make_float2(ex2(q.x), ex2(q.y)));
       }
     }
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     z_edge = Log<T>::get(zs + sl.edge(tid));
     if (!kTail || !marked(sl.edge(tid))) {
       raise(z_edge);
-      s2.x += ex2(fmaf(z_edge, P.c2, -r1.m2));
+      s2.x += ex2_from(z_edge, ref(r1.m), P.c2);
     }
   }
   if (gs) batch(x, 0);  // the second pass's first batch
@@ -477,18 +482,16 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   // the listed entries: their teacher's maximum and sum, or with a rest class
   // their student's exponentials, and the sum of p in float64 (1 - sum p may be
   // small)
-  Run1 r2 = {kNegInf, 0.f, 0.f};
+  Run1 r2 = {kNegInf, 0.f};
   double p_sum = 0.0;
   const double lse2_t = kTail ? (double)P.t_lse[row] * 1.4426950408889634 : 0.0;
   for_entries([&](int, float t, float z) {
     const float l = kTail ? z : t;
     if (l > r2.m) {
-      const float n2 = __fmul_rn(l, P.c2);
-      r2.s = r2.m == kNegInf ? 0.f : r2.s * ex2(r2.m2 - n2);
+      r2.s *= ex2_from(r2.m, l, P.c2);
       r2.m = l;
-      r2.m2 = n2;
     }
-    r2.s += ex2(fmaf(l, P.c2, -r2.m2));
+    r2.s += ex2_from(l, ref(r2.m), P.c2);
     if (kTail) p_sum += (double)ex2((float)log2p(t, P.c2d, lse2_t));
   });
   r1 = warp_join(r1, P.c2);
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float m = lane < kWarps ? sm_m[j][lane] : kNegInf, mm = warp_max(m);
-      const float f = m == kNegInf ? 0.f : ex2(__fmul_rn(m, P.c2) - __fmul_rn(mm, P.c2));
+      const float f = m == kNegInf ? 0.f : ex2_from(m, mm, P.c2);
       d[j] = warp_sum(m == kNegInf ? 0.0 : (double)(sm_s[j][lane] * f));
       (j ? p.m2nd : p.m) = mm;
     }
@@ -529,42 +532,39 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       M = fmaxf(M, parts[r].m);
       M2nd = fmaxf(M2nd, parts[r].m2nd);
     }
-    const float M2 = M == kNegInf ? 0.f : __fmul_rn(M, P.c2);
-    const float N2 = M2nd == kNegInf ? 0.f : __fmul_rn(M2nd, P.c2);
-    auto scaled = [&](float m, double v, float to2) {
+    auto scaled = [&](float m, double v, float to) {
       if (m == kNegInf) return 0.0;
-      const float d = __fmul_rn(m, P.c2) - to2;
-      return d == 0.f ? v : v * exp2((double)d);
+      return m == to ? v : v * exp2(((double)m - (double)to) * (double)P.c2);
     };
     double second = 0.0;
     for (int r = 0; r < n_parts; ++r) {
-      S += scaled(parts[r].m, parts[r].s, M2);
-      second += scaled(parts[r].m2nd, parts[r].s2nd, N2);
+      S += scaled(parts[r].m, parts[r].s, M);
+      second += scaled(parts[r].m2nd, parts[r].s2nd, M2nd);
       TS += parts[r].p_sum;
     }
     RowNumbers n;
     if (kTail) {
       // both sums in units of the larger maximum
-      const float top2 = M2nd == kNegInf || M > M2nd ? M2 : N2;
-      to_top = (double)M2 - (double)top2;
+      const float top = fmaxf(M, M2nd);
+      to_top = M == top ? 0.0 : ((double)M - (double)top) * (double)P.c2;
       const float up = to_top == 0.0 ? 1.f : exp2f((float)to_top);
-      total = (M == kNegInf ? S : S * (double)up) + scaled(M2nd, second, top2);
+      total = S * (double)up + scaled(M2nd, second, top);
       // nothing outside the list: no rest class, neither in the loss nor in its gradient
       R = S > 0.0 && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
       const double C = TS + R;
       const float scale = w * P.inv_temp, f = (float)C / (float)total;
-      n.m2 = top2;
-      n.r2 = M2;
+      n.m = ref(top);
+      n.m_rest = ref(M);
       n.f_rest = S > 0.0 ? scale * (f * up - (float)R / (float)S) : 0.f;
       n.f_top = scale * f;
-      n.inv_ts = n.tm2 = 0.f;
+      n.inv_ts = n.tm = 0.f;
     } else {
       total = S;
       TS = second;
-      n.m2 = n.r2 = M2;
+      n.m = n.m_rest = ref(M);
       n.f_rest = n.f_top = TS > 0.0 ? w * P.inv_temp / (float)total : 0.f;
       n.inv_ts = TS > 0.0 ? 1.f / (float)TS : 0.f;
-      n.tm2 = N2;
+      n.tm = ref(M2nd);
     }
     row_n = n;
   }
@@ -579,14 +579,14 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 
   // second pass: the gradient of entries that are not listed
   if (gs) {
-    const float2 fr = make_float2(n.f_rest, n.f_rest), nn = make_float2(-n.r2, -n.r2);
+    const float2 fr = make_float2(n.f_rest, n.f_rest), nn = make_float2(-n.m_rest, -n.m_rest);
     uint4* out = reinterpret_cast<uint4*>(gs) + sl.v_lo + tid;
     auto grad = [&](const uint4& x) {
       float f[kE];
       Log<T>::unpack(x, f);
 #pragma unroll
       for (int i = 0; i < kE; i += 2) {
-        float2 y = ffma2(make_float2(f[i], f[i + 1]), c2v, nn);
+        float2 y = fmul2(fadd2(make_float2(f[i], f[i + 1]), nn), c2v);
         y = fmul2(make_float2(ex2(y.x), ex2(y.y)), fr);
         f[i] = y.x;
         f[i + 1] = y.y;
@@ -613,30 +613,33 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       for (int u = 0; u < kUnroll; ++u) x[u] = y[u];
     }
     if (tid < sl.n_edge)
-      Log<T>::put(gs + sl.edge(tid), n.f_rest * ex2(fmaf(z_edge, P.c2, -n.r2)));
+      Log<T>::put(gs + sl.edge(tid), n.f_rest * ex2_from(z_edge, n.m_rest, P.c2));
     __syncthreads();
   }
   // The listed entries: their gradients over it, and the loss up to the
   // logarithms of the sums: sum p (log2 p - log2 q) = sum p (a - b) + sum p lg,
   // a and b the exponents of p and q relative to their references, in float64
-  // (the logits may be far larger than the difference).
+  // (the logits may be far larger than the difference, and the difference past
+  // float32's range).
   const float scale = w * P.inv_temp;
-  float part = 0.f, mass = 0.f;
+  double part = 0.0;
+  float mass = 0.f;
   for_entries([&](int e, float t, float z) {
     // without a rest class the teacher's exponents, as the student's, use the
     // rounded c2: both sides of their log-partitions then agree
-    const double a = kTail ? log2p(t, P.c2d, lse2_t) : (double)t * (double)P.c2 - (double)n.tm2;
+    const double a = kTail ? log2p(t, P.c2d, lse2_t) : ((double)t - (double)n.tm) * (double)P.c2;
     const float p = kTail ? ex2((float)a) : n.inv_ts > 0.f ? ex2((float)a) * n.inv_ts : 0.f;
     if (p != 0.f) {
-      part = fmaf(p, (float)(a - ((double)z * (double)P.c2 - (double)n.m2)), part);
+      part += (double)p * (a - ((double)z - (double)n.m) * (double)P.c2);
       mass += p;
     }
     if (gs && LQ_IN_RANGE(sl.c0 + e, P.V))
-      Log<T>::put(gs + e, n.f_top * ex2(fmaf(z, P.c2, -n.m2)) - scale * p);
+      Log<T>::put(gs + e, n.f_top * ex2_from(z, n.m, P.c2) - scale * p);
   });
   {
-    const float pf = warp_sum(part), mf = warp_sum(mass);
-    if (lane == 0) sm_d[0][warp] = pf, sm_d[1][warp] = mf;
+    const double pd = warp_sum(part);
+    const float mf = warp_sum(mass);
+    if (lane == 0) sm_d[0][warp] = pd, sm_d[1][warp] = mf;
   }
   __syncthreads();
   if (warp == 0) {

@@ -433,8 +433,8 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *   grad    = d loss[m] / d z, of the loss as returned: where the R term is left
  *       out of the loss it is left out of the gradient.
  *   d_logits    M x V, dtype LQ_F32, LQ_BF16 or LQ_F16; entries may be -inf
- *               (masked vocabulary), not all of a row.  Rows start anywhere: V is
- *               arbitrary.
+ *               (masked vocabulary), not all of a row, or any finite value, the
+ *               type's lowest included.  Rows start anywhere: V is arbitrary.
  *   d_t_values  M x k, t_dtype any of the three types; -inf counts nothing.
  *   d_t_index   M x k vocabulary indices, int32 (idx_bytes 4) or int64 (8).  An
  *               index outside [0, V) is no entry (padding of a shorter list);

@@ -31,6 +31,13 @@ def rand(seed, *shape, scale=1.0):
     return torch.randn(shape, generator=g, device="cuda") * scale
 
 
+def log_sum(y):
+    """log sum exp(y) as (m, l), m + l: apart, or l is lost beside an m of 1e38, and
+    with it the gradient."""
+    m = y.detach().max()
+    return m, torch.log(torch.exp(y - m).sum())
+
+
 def row_oracle(z, tv, ti, t_lse, w, temp):
     """One row: (loss, grad, tolerance of each but for the last rounding)."""
     V = z.numel()
@@ -49,20 +56,20 @@ def row_oracle(z, tv, ti, t_lse, w, temp):
     t = torch.tensor(val, dtype=torch.float64)
     R = 0.0
     if t_lse is None:
-        log_p = torch.log_softmax(t, 0)
+        log_p = t - t.max() - log_sum(t)[1]
     else:
         log_p = t - t_lse
         R = max(0.0, 1.0 - float(log_p.exp().sum()))
     p = log_p.exp()
-    lse = torch.logsumexp(y, 0)
+    m, l = log_sum(y)
     on = p > 0
-    log_q = y[idx][on] - lse
+    log_q = y[idx][on] - m - l
     loss = (p[on] * (log_p[on] - log_q)).sum()
     rest = y[~hidden]
     log_Q = torch.tensor(0.0)
     if R > 0 and bool((rest > -math.inf).any()):
-        lse_rest = torch.logsumexp(rest, 0)
-        log_Q = lse_rest - lse
+        m_rest, l_rest = log_sum(rest)
+        log_Q = m_rest - m + l_rest - l
         loss = loss + R * (math.log(R) - log_Q)
     else:
         R = 0.0
@@ -74,13 +81,13 @@ def row_oracle(z, tv, ti, t_lse, w, temp):
         tl += float((p[on] * (2.0 ** -22 + 2.0 ** -23 * log_p[on].abs()) *
                      (log_p[on] - log_q).abs()).sum())
         C = float(p.sum()) + R
-        q = (y - lse).exp()
+        q = (y - m - l).exp()
         tg = C * q * (2.0 ** -18 + 2.0 ** -22 * (y.max() - y).clamp(max=1e4))
         tg[idx] += p * (2.0 ** -21 + 2.0 ** -22 * log_p.clamp(min=-1e4).abs())
         if R:
             size = abs(math.log(R)) + abs(float(log_Q))
             tl += R * (2.0 ** -18 + 2.0 ** -23 * size) + D_R * (2 + size)
-            s = torch.where(hidden, zero, (y - lse_rest).exp())
+            s = torch.where(hidden, zero, (y - m_rest - l_rest).exp())
             tg += s * (R * (2.0 ** -18 + 2.0 ** -22 * (rest.max() - y).clamp(0, 1e4)) + D_R)
     return w * float(loss.detach()), g * w, abs(w) * tl, abs(w) / temp * tg
 
@@ -202,3 +209,61 @@ def test_masked_entries_next_to_ordinary_ones(name):
     for lse in (None, torch.logsumexp(teacher, 1)):
         loss, grad = check(z, tv, ti, t_lse=lse)
         assert not grad[z == -math.inf].any()
+
+
+def lowest(dt):
+    return torch.finfo(dt).min
+
+
+@pytest.mark.parametrize("M,V,k", [(3, 1000, 64), (2, 49152, 64), (300, 8001, 20)])
+@pytest.mark.parametrize("name", TYPES)
+@pytest.mark.parametrize("temp", [0.5, 1.0, 3.0])
+def test_blocks_masked_with_the_lowest_value(M, V, k, name, temp):
+    """A padded vocabulary, or whole regions, masked with the type's lowest value: the
+    threads that see nothing else count nothing."""
+    dt = TYPES[name]
+    for lo, hi in ((V - V // 5, V), (0, V // 3), (V // 4, V // 2)):
+        z, tv, ti, lse = apart(V + lo, M, V, k, dt, 3.0, 0.2)
+        mask = torch.zeros(M, V, dtype=torch.bool, device="cuda")
+        mask[:, lo:hi] = True
+        mask.scatter_(1, ti, False)
+        z = torch.where(mask, torch.full_like(z, lowest(dt)), z)
+        lse = (torch.logsumexp(tv.double() / temp, 1) - math.log(0.8)).float()
+        for t_lse in (None, lse):
+            loss, grad = check(z, tv, ti, t_lse=t_lse, temp=temp, rows=(0, M - 1))
+            assert not grad[mask].any() and not loss.isnan().any()
+
+
+@pytest.mark.parametrize("M,V", [(3, 1000), (2, 49152)])
+def test_rows_of_nothing_but_the_lowest_value(M, V):
+    """Equal logits are a uniform distribution wherever they lie, the teacher's too;
+    masked with the lowest value outside the list, the rest class costs R times the
+    distance."""
+    for name, dt in TYPES.items():
+        z, tv, ti, lse = apart(V, M, V, 30, dt, 0.0, 0.3)
+        flat = torch.full_like(z, lowest(dt))
+        for t_lse in (None, lse.float()):
+            check(flat, tv, ti, t_lse=t_lse)
+        check(z, torch.full_like(tv, lowest(torch.float32)), ti)
+        check(z, torch.full_like(tv, lowest(dt)).to(dt), ti)
+        check(torch.full_like(z, lowest(dt)).scatter(1, ti, z.gather(1, ti)), tv, ti,
+              t_lse=lse.float())
+        # a listed logit that is masked while the teacher gives it mass
+        check(z.scatter(1, ti[:, :1], lowest(dt)), tv, ti)
+        check(z.scatter(1, ti[:, :1], lowest(dt)), tv, ti, t_lse=lse.float())
+        top = z.clone()
+        top[:, V // 2:] = -lowest(dt) / 2  # and the far side: most of the mass up there
+        top[:, :V // 2] = lowest(dt)
+        check(top, tv, ti, t_lse=lse.float())
+
+
+def test_small_temperatures():
+    """logits over the temperature past float32's range."""
+    z, tv, ti, lse = apart(1, 3, 1000, 20, torch.float32, 0.0, 0.3)
+    for temp in (1e-3, 1e-10, 1e-30):
+        scaled = z * temp
+        scaled[:, 500:] = -1e37
+        scaled = scaled.scatter(1, ti, (z * temp).gather(1, ti))
+        for t_lse in (None, lse.float()):
+            loss, grad = check(scaled, tv * temp, ti, t_lse=t_lse, temp=temp)
+            assert not loss.isinf().any()
