@@ -240,7 +240,9 @@ struct RowNumbers {
 // and the maximum, times c2: z c2 - m c2 would be one multiply-add, but both products
 // leave float32's range where logits are masked with their type's lowest value or the
 // temperature is small, and inf - inf is no number.  The difference may at worst be
-// -inf, which counts nothing.  ref: the maximum, 0 while there is none.
+// -inf, which counts nothing.  ref: the maximum, 0 while there is none.  A maximum
+// passes over NaN, a sum does not: where nothing but NaN was seen m is -inf and s NaN,
+// and every join keeps it, so that the row's loss and gradient become NaN.
 struct Run1 {
   float m, s;
 };
@@ -251,7 +253,7 @@ __device__ __forceinline__ float ex2_from(float z, float from, float c2) {
 // the lanes' as one, in a fixed order
 __device__ __forceinline__ Run1 warp_join(Run1 r, float c2) {
   const float m = warp_max(r.m);
-  const float s = warp_sum(r.m == kNegInf ? 0.f : r.s * ex2_from(r.m, m, c2));
+  const float s = warp_sum(r.m == kNegInf ? r.s : r.s * ex2_from(r.m, m, c2));
   return {m, s};
 }
 
@@ -510,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, kCtas)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float m = lane < kWarps ? sm_m[j][lane] : kNegInf, mm = warp_max(m);
-      const float f = m == kNegInf ? 0.f : ex2_from(m, mm, P.c2);
-      d[j] = warp_sum(m == kNegInf ? 0.0 : (double)(sm_s[j][lane] * f));
+      const float f = m == kNegInf ? 1.f : ex2_from(m, mm, P.c2);
+      d[j] = warp_sum(lane < kWarps ? (double)(sm_s[j][lane] * f) : 0.0);
       (j ? p.m2nd : p.m) = mm;
     }
     p.s = d[0];
@@ -533,8 +535,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       M2nd = fmaxf(M2nd, parts[r].m2nd);
     }
     auto scaled = [&](float m, double v, float to) {
-      if (m == kNegInf) return 0.0;
-      return m == to ? v : v * exp2(((double)m - (double)to) * (double)P.c2);
+      return m == kNegInf || m == to ? v : v * exp2(((double)m - (double)to) * (double)P.c2);
     };
     double second = 0.0;
     for (int r = 0; r < n_parts; ++r) {
@@ -550,20 +551,21 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       const float up = to_top == 0.0 ? 1.f : exp2f((float)to_top);
       total = S * (double)up + scaled(M2nd, second, top);
       // nothing outside the list: no rest class, neither in the loss nor in its gradient
-      R = S > 0.0 && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
+      R = S != 0.0 && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
       const double C = TS + R;
       const float scale = w * P.inv_temp, f = (float)C / (float)total;
       n.m = ref(top);
       n.m_rest = ref(M);
-      n.f_rest = S > 0.0 ? scale * (f * up - (float)R / (float)S) : 0.f;
+      n.f_rest = S != 0.0 ? scale * (f * up - (float)R / (float)S) : 0.f;
       n.f_top = scale * f;
       n.inv_ts = n.tm = 0.f;
     } else {
       total = S;
       TS = second;
       n.m = n.m_rest = ref(M);
-      n.f_rest = n.f_top = TS > 0.0 ? w * P.inv_temp / (float)total : 0.f;
-      n.inv_ts = TS > 0.0 ? 1.f / (float)TS : 0.f;
+      n.inv_ts = TS != 0.0 ? 1.f / (float)TS : 0.f;
+      const float C = TS > 0.0 ? 1.f : (float)TS;  // the sum of p: 1, 0 without any, or NaN
+      n.f_rest = n.f_top = w * P.inv_temp / (float)total * C;
       n.tm = ref(M2nd);
     }
     row_n = n;
@@ -628,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     // without a rest class the teacher's exponents, as the student's, use the
     // rounded c2: both sides of their log-partitions then agree
     const double a = kTail ? log2p(t, P.c2d, lse2_t) : ((double)t - (double)n.tm) * (double)P.c2;
-    const float p = kTail ? ex2((float)a) : n.inv_ts > 0.f ? ex2((float)a) * n.inv_ts : 0.f;
+    const float p = kTail ? ex2((float)a) : n.inv_ts != 0.f ? ex2((float)a) * n.inv_ts : 0.f;
     if (p != 0.f) {
       part += (double)p * (a - ((double)z - (double)n.m) * (double)P.c2);
       mass += p;

@@ -434,7 +434,9 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *       out of the loss it is left out of the gradient.
  *   d_logits    M x V, dtype LQ_F32, LQ_BF16 or LQ_F16; entries may be -inf
  *               (masked vocabulary), not all of a row, or any finite value, the
- *               type's lowest included.  Rows start anywhere: V is arbitrary.
+ *               type's lowest included.  A NaN, here or among a row's teacher
+ *               values, makes that row's loss and gradient NaN.  Rows start
+ *               anywhere: V is arbitrary.
  *   d_t_values  M x k, t_dtype any of the three types; -inf counts nothing.
  *   d_t_index   M x k vocabulary indices, int32 (idx_bytes 4) or int64 (8).  An
  *               index outside [0, V) is no entry (padding of a shorter list);

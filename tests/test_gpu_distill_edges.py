@@ -267,3 +267,31 @@ def test_small_temperatures():
         for t_lse in (None, lse.float()):
             loss, grad = check(scaled, tv * temp, ti, t_lse=t_lse, temp=temp)
             assert not loss.isinf().any()
+
+
+@pytest.mark.parametrize("M,V,k", [(3, 100, 7), (2, 1000, 64), (2, 49152, 64), (300, 20011, 20)])
+@pytest.mark.parametrize("name", TYPES)
+def test_not_a_number_reaches_the_loss(M, V, k, name):
+    """A NaN among the logits makes its row's loss and gradient NaN, wherever it is and
+    also where a whole block of them fills a thread; NaN among the teacher's values
+    likewise.  Other rows are as without it."""
+    dt = TYPES[name]
+    z, tv, ti, lse = apart(V, M, V, k, dt, 1.0, 0.3)
+    nan = float("nan")
+    for t_lse in (None, lse.float()):
+        want = lq.lq_distill_loss(z[:1].clone(), tv[:1].clone(), ti[:1].clone(), want_grad=True,
+                                  t_lse=None if t_lse is None else t_lse[:1].clone())
+        for lo, hi in ((50, 51), (V - 1, V), (16, 48), (0, V)):
+            bad = z.clone()
+            bad[1, lo:hi] = nan
+            loss, grad = lq.lq_distill_loss(bad, tv, ti, t_lse=t_lse, want_grad=True)
+            assert loss[1].isnan() and grad[1].isnan().all(), (lo, hi)
+            assert not loss[0].isnan() and not grad[0].isnan().any()
+            if M == 3 and V == 100:  # the row alone is cut as in the batch
+                assert torch.equal(loss[:1], want[0]) and torch.equal(grad[:1], want[1])
+        for n in (1, k):
+            badt = tv.clone()
+            badt[1, :n] = nan
+            loss, grad = lq.lq_distill_loss(z, badt, ti, t_lse=t_lse, want_grad=True)
+            assert loss[1].isnan() and not loss[0].isnan()
+            assert grad[1].gather(0, ti[1, :n]).isnan().all()
