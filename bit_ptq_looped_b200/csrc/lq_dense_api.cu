@@ -316,8 +316,9 @@ lq_status lq_distill_loss(const void* d_logits, int32_t dtype, int64_t M, int64_
     set_error("invalid shape M=%lld V=%lld k=%lld", (long long)M, (long long)V, (long long)k);
     return LQ_ERR_ARG;
   }
-  if (!(temp > 0.f) || !std::isfinite(temp) || !std::isfinite(1.f / temp)) {
-    set_error("the temperature must be positive and finite");
+  // exponents are differences of logits times log2(e) / temp
+  if (!(temp > 0.f) || !std::isfinite(temp) || !std::isfinite(1.4426950408889634f / temp)) {
+    set_error("the temperature must be positive and finite, log2(e) over it too");
     return LQ_ERR_ARG;
   }
   const int64_t esz = dtype == LQ_F32 ? 4 : 2, tsz = t_dtype == LQ_F32 ? 4 : 2;

@@ -448,7 +448,8 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *   d_loss      out M float32;  d_grad  out M x V of dtype, or NULL; it may be
  *               d_logits itself (in place), no other overlap.
  * 1 <= k <= min(V, LQ_DISTILL_MAX_K) and V <= LQ_DISTILL_MAX_V (LQ_ERR_SHAPE);
- * temp > 0.  A thread and a warp sum in float32, a row in float64.  Asynchronous
+ * temp > 0, it and log2(e) / temp finite in float32 (LQ_ERR_ARG).  A thread and a
+ * warp sum in float32, a row in float64.  Asynchronous
  * on `stream`; safe to capture; two runs of a call give the same bits.
  */
 #define LQ_DISTILL_MAX_K 8192

@@ -1,0 +1,26 @@
+"""Host-side checks of the dense entry points and the distillation loss at the ends of
+what they accept (no GPU needed)."""
+import pytest
+
+from bit_ptq_looped_b200 import build as B
+from bit_ptq_looped_b200 import lq
+
+X, W, Y, Z = ((i + 1) << 40 for i in range(4))  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return lq.lib()
+
+
+def test_temperatures_whose_exponent_factor_is_not_finite_are_refused(L):
+    """log2(e) / temp scales every exponent; at 3.5e-39 one over the temperature is
+    finite in float32 (2.86e38) and this factor is not."""
+    def call(temp):
+        return L.lq_distill_loss(X, lq.LQ_F32, 4, 100, W, lq.LQ_F32, Z, 8, 5, None, None, temp, Y,
+                                 None, None)
+
+    for temp in (3.5e-39, 4.2e-39):
+        assert call(temp) == lq.LQ_ERR_ARG
+        assert "temperature" in L.lq_last_error().decode()
