@@ -1146,8 +1146,9 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_dense_rows(const RowsParams
     uint4 a[kRowsUnroll][kF][2], xb[kRowsUnroll][kNT];
 #pragma unroll
     for (int u = 0; u < kRowsUnroll; ++u) {
-      const int k = (b0 + u * kRowsWarps) * 32 + 8 * t;
-      const bool in = k < P.K;  // K is a multiple of 8
+      // up to 48 blocks past the last one, which may pass 2^31: compared unsigned
+      const int k = (int)((uint32_t)(b0 + u * kRowsWarps) * 32u) + 8 * t;
+      const bool in = (uint32_t)k < (uint32_t)P.K;  // K is a multiple of 8
 #pragma unroll
       for (int f = 0; f < kF; ++f)
 #pragma unroll

@@ -449,8 +449,8 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *               d_logits itself (in place), no other overlap.
  * 1 <= k <= min(V, LQ_DISTILL_MAX_K) and V <= LQ_DISTILL_MAX_V (LQ_ERR_SHAPE);
  * temp > 0, it and log2(e) / temp finite in float32 (LQ_ERR_ARG).  A thread and a
- * warp sum in float32, a row in float64.  Asynchronous
- * on `stream`; safe to capture; two runs of a call give the same bits.
+ * warp sum in float32, a row in float64.  Asynchronous on `stream`; safe to
+ * capture; two runs of a call give the same bits.
  */
 #define LQ_DISTILL_MAX_K 8192
 #define LQ_DISTILL_MAX_V (512 * 1024)
