@@ -1737,7 +1737,7 @@ Shape pick_shape(int64_t M, int64_t N, int n_kb, int factors, int max_slices, bo
   for (int members = 2; may_share && members <= 4 && tiles * members <= sms; members *= 2) {
     const int kb = (n_kb + members - 1) / members;
     if ((members - 1) * kb >= n_kb) break;  // every member has a part
-    const int64_t c = kb * 285 + 2600 + 5000;
+    const int64_t c = (int64_t)kb * 285 + 2600 + 5000;
     if (c < best.clocks) best = {64, 1, members, c};
   }
   return best;

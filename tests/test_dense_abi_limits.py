@@ -24,3 +24,14 @@ def test_temperatures_whose_exponent_factor_is_not_finite_are_refused(L):
     for temp in (3.5e-39, 4.2e-39):
         assert call(temp) == lq.LQ_ERR_ARG
         assert "temperature" in L.lq_last_error().decode()
+
+
+def test_workspace_sizes_at_the_longest_contractions(L):
+    """Contractions of up to 2^31: the block times that choose a tile shape are sums of
+    64-bit terms (the sanitizer build reports an overflow)."""
+    for M, N, K in ((8, 2 ** 31 - 256, 8), (16, 2 ** 30 + 8, 64), (2 ** 31 - 256, 64, 8),
+                    (100, 8, 2 ** 31 - 256)):
+        n = L.lq_dense_linear_bwd_workspace_bytes(M, N, K, lq.LQ_ACT_SILU)
+        assert n >= 2 * M * N and n % 256 == 0
+        n = L.lq_gated_linear_bwd_workspace_bytes(M, N, K)
+        assert n >= 4 * M * N and n % 256 == 0
