@@ -1956,18 +1956,21 @@ cudaError_t backward(const DenseBackward& d, cudaStream_t s) {
     e = run_grad<T, false, true>(dx_shape(d.M, half, d.K, gated), a, a2, b, b2, P, false, slices, s);
     if (e != cudaSuccess) return e;
   }
-  if (d.dw || d.dw2) {
-    // output rows: the columns of dz; the padding columns between and after
-    // the factors are not written.  A factor that is not wanted is left out.
-    const bool only2 = !d.dw;
-    const int64_t rows = gated && d.dw && d.dw2 ? half + d.N : d.N;
+  // Output rows of a weight gradient: the columns of dz.  Both factors are one
+  // product, whose padding rows between and after them are not written, unless its
+  // rows pass the 31 bits of a TMA coordinate.
+  const bool both = d.dw && d.dw2 && half + d.N <= INT32_MAX - 255;
+  for (int f = 0; f < 2; ++f) {
+    void* dw = f ? d.dw2 : d.dw;
+    if (!dw || (f && both)) continue;
+    const int64_t rows = both ? half + d.N : d.N;
     GemmParams P = base_params(rows, d.K, d.M);
-    P.out = only2 ? d.dw2 : d.dw;
-    P.out2 = d.dw2;
+    P.out = dw;
+    P.out2 = both ? d.dw2 : nullptr;
     P.rows1 = d.N;
-    P.split = rows > d.N ? half : rows;
+    P.split = both ? half : rows;
     P.accumulate = d.accumulate;
-    const Operand a{only2 ? (const void*)(dz + half) : dzp, rows, d.M, pl.ldz};
+    const Operand a{f ? (const void*)(dz + half) : dzp, rows, d.M, pl.ldz};
     const Operand b{d.x, d.K, d.M, d.K};
     e = run_grad<T, true, true>(dw_shape(rows, d.K, d.M), a, a, b, b, P, d.f32, slices, s);
     if (e != cudaSuccess) return e;
