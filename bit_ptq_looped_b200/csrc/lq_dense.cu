@@ -78,6 +78,12 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   }
 }
 
+// The same wait by a whole warp, with one answer: lanes may see the limit or the abort
+// flag at different polls, and what follows (tcgen05.ld, shuffles) needs all of them.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(~0u, wait_bounded(bar, parity, abort));
+}
+
 // The same wait without the abort flag (teardown: no copy or MMA of this CTA is
 // in flight when it exits).
 __device__ __forceinline__ void wait_drain(uint32_t bar, uint32_t parity) {
@@ -930,7 +936,7 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi, kShared>::kThreads, 1)
     int im, in;
     tile_at(t_first, tm, tn, im, in);
     shared.load(P, member, (int64_t)im * kTileM, (int64_t)in * kTileN);
-    const bool ok = __all_sync(~0u, wait_bounded(bar_accf, 0u, abort_flag));
+    const bool ok = wait_warp(bar_accf, 0u, abort_flag);
     cluster_wait();  // every member runs, so that its shared memory may be written
     if (ok && (int64_t)im * kTileM + 32 * warp < P.M) {
       tc_fence_after();
@@ -973,7 +979,7 @@ __global__ void __launch_bounds__(Cfg<kBN, kPair, kEpi, kShared>::kThreads, 1)
         for (int i = 1; i < kParts; ++i) b = k == i ? o[i] : b;
         return b;
       };
-      if (!wait_bounded(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag)) break;
+      if (!wait_warp(bar_accf + 8 * buf, (uint32_t)(j >> 1) & 1u, abort_flag)) break;
       tc_fence_after();
       const uint32_t acc = tmem_base + ((uint32_t)(32 * q) << 16) +
                            (uint32_t)(buf * kBN + part * C::kCols);
