@@ -1412,6 +1412,16 @@ lq_status lq_selftest_bounded_wait(int64_t limit_us, void* stream) {
   return LQ_OK;
 }
 
+lq_status lq_selftest_dense_wait(int64_t limit_us, void* stream) {
+  if (limit_us <= 0 || limit_us > 10000000) {
+    set_error("limit must be in (0, 10 s]");
+    return LQ_ERR_ARG;
+  }
+  cudaError_t e = launch_dense_wait_selftest((uint64_t)limit_us * 1000u, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_error(e, "self-test launch");
+  return LQ_OK;
+}
+
 lq_status lq_selftest_grid_wait(int64_t limit_us, void* d_scratch, void* stream) {
   if (limit_us <= 0 || limit_us > 10000000) {
     set_error("limit must be in (0, 10 s]");
@@ -1431,8 +1441,10 @@ lq_status lq_check_device(void* stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_error(e, "pending CUDA error");
   lq_status st = read_and_clear_device_status((cudaStream_t)stream);
-  const int dense = take_dense_status();  // one report covers all status words
+  int dense = 0;
+  e = take_dense_status(&dense);  // one report covers all status words
   if (st != LQ_OK) return st;
+  if (e != cudaSuccess) return cuda_error(e, "read the dense kernels' status");
   if (dense != 0) {
     set_error("a bounded device-side wait expired in a dense kernel (status %d)", dense);
     return (lq_status)dense;

@@ -59,7 +59,8 @@ __device__ int g_dense_status = 0;
 // Bounded wait on an mbarrier phase: false once `limit_ns` have passed or the
 // CTA's abort flag is up (and raises it on a timeout, so that the other roles
 // stop too).  The clock is read once in 1024 polls.
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort,
+                                             uint64_t limit_ns = kWaitLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = 0;
   for (uint32_t i = 1;; ++i) {
@@ -69,7 +70,7 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
       const uint64_t t = global_timer_ns();
       if (t0 == 0) {
         t0 = t;
-      } else if (t - t0 > kWaitLimitNs) {
+      } else if (t - t0 > limit_ns) {
         *abort = 1;
         atomicExch(&g_dense_status, (int)LQ_ERR_DEVICE_TIMEOUT);
         return false;
@@ -80,8 +81,9 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
 
 // The same wait by a whole warp, with one answer: lanes may see the limit or the abort
 // flag at different polls, and what follows (tcgen05.ld, shuffles) needs all of them.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(~0u, wait_bounded(bar, parity, abort));
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          uint64_t limit_ns = kWaitLimitNs) {
+  return __all_sync(~0u, wait_bounded(bar, parity, abort, limit_ns));
 }
 
 // The same wait without the abort flag (teardown: no copy or MMA of this CTA is
@@ -1605,6 +1607,21 @@ __global__ void __launch_bounds__(256) k_rows_dw(const RowsBwdParams P) {
   }
 }
 
+// Self-test of the waits: a warp waits on an mbarrier phase that nothing completes, as
+// an epilogue warp does, and gives up after limit_ns.
+__global__ void __launch_bounds__(32) k_dense_wait_selftest(uint64_t limit_ns) {
+  __shared__ __align__(8) unsigned long long bar;
+  __shared__ int abort_flag;
+  const uint32_t b = smem_u32(&bar);
+  if (threadIdx.x == 0) {
+    mbar_init(b, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncwarp();
+  wait_warp(b, 0u, &abort_flag, limit_ns);
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
@@ -2020,11 +2037,17 @@ cudaError_t launch_dense_backward(const DenseBackward& d, cudaStream_t s) {
 
 unsigned long long bounds_fail_dense() { return lq_take_bounds_fail(); }
 
-int take_dense_status() {
-  int v = 0, zero = 0;
-  if (cudaMemcpyFromSymbol(&v, g_dense_status, sizeof(int)) != cudaSuccess) return 0;
-  if (v) cudaMemcpyToSymbol(g_dense_status, &zero, sizeof(int));
-  return v;
+cudaError_t launch_dense_wait_selftest(uint64_t limit_ns, cudaStream_t s) {
+  k_dense_wait_selftest<<<1, 32, 0, s>>>(limit_ns);
+  return cudaGetLastError();
+}
+
+cudaError_t take_dense_status(int* status) {
+  int zero = 0;
+  *status = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(status, g_dense_status, sizeof(int));
+  if (e == cudaSuccess && *status) e = cudaMemcpyToSymbol(g_dense_status, &zero, sizeof(int));
+  return e;
 }
 
 }  // namespace lq

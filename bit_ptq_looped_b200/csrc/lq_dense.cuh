@@ -62,8 +62,9 @@ struct DistillArgs {
 cudaError_t launch_distill(const DistillArgs& a, cudaStream_t s);
 
 // the dense kernels' status word (LQ_ERR_DEVICE_TIMEOUT after a bounded wait
-// expired), read and cleared
-int take_dense_status();
+// expired), read and cleared; an error where it could not be
+cudaError_t take_dense_status(int* status);
+cudaError_t launch_dense_wait_selftest(uint64_t limit_ns, cudaStream_t s);
 
 // per source file: the first index out of range of the bounds-check build (0: none)
 unsigned long long bounds_fail_dense();

@@ -76,6 +76,7 @@ SIGNATURES = {
                                _vp, _vp, _vp]),
     "lq_check_device": (_i32, [_vp]),
     "lq_selftest_bounded_wait": (_i32, [_i64, _vp]),
+    "lq_selftest_dense_wait": (_i32, [_i64, _vp]),
     "lq_selftest_grid_wait": (_i32, [_i64, _vp, _vp]),
     "lq_loop_linear_noalloc": (_i32, [_vp, _i32, _i64, _vp, _i32, _vp, _vp]),
     "lq_probe_enable": (_i32, [_i32]),
@@ -709,6 +710,10 @@ def lq_probe_read() -> dict:
 
 def lq_selftest_bounded_wait(limit_us: int = 1000, stream=None) -> None:
     _check(lib().lq_selftest_bounded_wait(limit_us, _stream(stream)), "lq_selftest_bounded_wait")
+
+
+def lq_selftest_dense_wait(limit_us: int = 1000, stream=None) -> None:
+    _check(lib().lq_selftest_dense_wait(limit_us, _stream(stream)), "lq_selftest_dense_wait")
 
 
 def lq_selftest_grid_wait(scratch: torch.Tensor, limit_us: int = 1000, stream=None) -> None:

@@ -528,6 +528,12 @@ lq_status lq_check_device(void* stream);
 lq_status lq_selftest_bounded_wait(int64_t limit_us, void* stream);
 
 /*
+ * lq_selftest_dense_wait -- the same diagnostic for the wait and the status word
+ * of the dense products' kernels: a warp waits as one of their epilogue warps does.
+ */
+lq_status lq_selftest_dense_wait(int64_t limit_us, void* stream);
+
+/*
  * lq_selftest_grid_wait -- the same diagnostic for the grid barrier of the
  * persistent chain-mode decode kernel: one block waits at a grid barrier that
  * expects one block more than the launch has.  The wait gives up after

@@ -35,3 +35,8 @@ def test_workspace_sizes_at_the_longest_contractions(L):
         assert n >= 2 * M * N and n % 256 == 0
         n = L.lq_gated_linear_bwd_workspace_bytes(M, N, K)
         assert n >= 4 * M * N and n % 256 == 0
+
+
+def test_selftest_rejects_bad_limits(L):
+    for bad in (0, -5, 10 ** 8):
+        assert L.lq_selftest_dense_wait(bad, None) == lq.LQ_ERR_ARG
