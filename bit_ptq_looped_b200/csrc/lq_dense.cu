@@ -548,12 +548,12 @@ __device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, c
     const int odd = ((uintptr_t)d & 2) ? 1 : 0;
     const int e = 2 * lane + odd;  // first element of this lane's word
     if (odd) w = __funnelshift_r(w, next, 16);
-    if (e + 1 < n) *reinterpret_cast<uint32_t*>(d + e) = w;
+    if (e + 1 < n && LQ_IN_RANGE(col0 + e + 1, N)) *reinterpret_cast<uint32_t*>(d + e) = w;
     // what no whole word covers: the first element, and the last where one is left
     const int tail = (n - odd) & 1;
-    if (lane == 0 && odd)
+    if (lane == 0 && odd && LQ_IN_RANGE(col0, N))
       d[0] = *reinterpret_cast<const uint16_t*>(stg + piece_at<kRowBytes>(row, 0));
-    if (lane == 1 && tail)
+    if (lane == 1 && tail && LQ_IN_RANGE(col0 + n - 1, N))
       d[n - 1] = *reinterpret_cast<const uint16_t*>(
           stg + piece_at<kRowBytes>(row, (n - 1) / 8) + ((n - 1) % 8) * 2);
   }
@@ -682,7 +682,7 @@ __device__ __forceinline__ void store8(uint16_t* row, int64_t c, int64_t N, bool
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e)
-    if (c + e < N) row[c + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+    if (c + e < N && LQ_IN_RANGE(c + e, N)) row[c + e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
 }
 
 // The elements at p[c] .. p[c + 7] that lie below n, zero beyond.
@@ -1208,16 +1208,17 @@ __global__ void __launch_bounds__(32 * kRowsWarps) k_dense_rows(const RowsParams
     }
     const int64_t o = (int64_t)m * P.N + n;
     if (P.bias) v[0] += Elem<T>::load(P.bias + n);
-    if (P.aux) P.aux[o] = Elem<T>::round(v[0]);
+    const bool ok = LQ_IN_RANGE(o, (int64_t)P.M * P.N);
+    if (P.aux && ok) P.aux[o] = Elem<T>::round(v[0]);
     apply_act(P.act, v);
     if (kGated) {
       if (P.bias2) s2 += Elem<T>::load(P.bias2 + n);
-      if (P.aux2) P.aux2[o] = Elem<T>::round(s2);
+      if (P.aux2 && ok) P.aux2[o] = Elem<T>::round(s2);
       v[0] *= s2;
     } else if (P.res) {
       v[0] += Elem<T>::load(P.res + o);
     }
-    if (LQ_IN_RANGE(o, (int64_t)P.M * P.N)) P.y[o] = Elem<T>::round(v[0]);
+    if (ok) P.y[o] = Elem<T>::round(v[0]);
   }
 }
 
@@ -1331,7 +1332,8 @@ __global__ void __launch_bounds__(256) k_act_grad(const GradParams P) {
     float s = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) s += red[k][f][c];
-    P.sums[((int64_t)blockIdx.y * kF + f) * P.N + col] = s;
+    const int64_t at = ((int64_t)blockIdx.y * kF + f) * P.N + col;
+    if (LQ_IN_RANGE(at, (int64_t)gridDim.y * kF * P.N)) P.sums[at] = s;
   }
 }
 
@@ -1349,6 +1351,7 @@ __global__ void __launch_bounds__(256) k_col_sums(const float* __restrict__ sums
   void* o = c < N ? out : out2;
   if (!o) return;
   const int64_t i = c < N ? c : c - N;
+  if (!LQ_IN_RANGE(i, N)) return;
   if (f32)
     ((float*)o)[i] = accumulate ? ((float*)o)[i] + s : s;
   else
@@ -1368,7 +1371,7 @@ __global__ void __launch_bounds__(256)
   const int64_t r = i / cols, c = i - r * cols;
   const RowMap map = {P.M, P.rows1, P.split, (char*)P.out, (char*)P.out2, cols * (f32 ? 4 : 2)};
   char* dst = map(r);
-  if (!dst) return;
+  if (!dst || !LQ_IN_RANGE(c + 3, cols)) return;
   float4 v = *reinterpret_cast<const float4*>(part + i);
   for (int k = 1; k < slices; ++k) {
     const float4 q = *reinterpret_cast<const float4*>(part + k * rows * cols + i);

@@ -376,8 +376,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
     if (rank == 0 && tid == 0) P.loss[row] = 0.f;
     if (!gs) return;
     for (int v = sl.v_lo + tid; v < sl.v_hi; v += kThreads)
-      reinterpret_cast<uint4*>(gs)[v] = make_uint4(0, 0, 0, 0);
-    if (tid < sl.n_edge) Log<T>::put(gs + sl.edge(tid), 0.f);
+      if (LQ_IN_RANGE(sl.c0 + (v + 1) * kE - 1, P.V))
+        reinterpret_cast<uint4*>(gs)[v] = make_uint4(0, 0, 0, 0);
+    if (tid < sl.n_edge && LQ_IN_RANGE(sl.c0 + sl.edge(tid), P.V))
+      Log<T>::put(gs + sl.edge(tid), 0.f);
   };
   // a row of weight 0 counts nothing, whatever its logits hold (the same
   // decision in every CTA of the cluster)
@@ -583,6 +585,10 @@ __global__ void __launch_bounds__(kThreads, kCtas)
   if (gs) {
     const float2 fr = make_float2(n.f_rest, n.f_rest), nn = make_float2(-n.m_rest, -n.m_rest);
     uint4* out = reinterpret_cast<uint4*>(gs) + sl.v_lo + tid;
+    // the row's column at which a vector starts (for the bounds-check build)
+    [[maybe_unused]] auto column = [&](int b, int u) {
+      return sl.c0 + (int64_t)(sl.v_lo + tid + (b * kUnroll + u) * kThreads) * kE;
+    };
     auto grad = [&](const uint4& x) {
       float f[kE];
       Log<T>::unpack(x, f);
@@ -603,18 +609,19 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       if (b < n_full) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (LQ_IN_RANGE(tid + (b * kUnroll + u) * kThreads, n_vec))
+          if (LQ_IN_RANGE(column(b, u) + kE - 1, P.V))
             __stcs(o + u * kThreads, grad(x[u]));
       } else {
         const int left = n_vec - tid - b * (kUnroll * kThreads);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (u * kThreads < left) __stcs(o + u * kThreads, grad(x[u]));
+          if (u * kThreads < left && LQ_IN_RANGE(column(b, u) + kE - 1, P.V))
+            __stcs(o + u * kThreads, grad(x[u]));
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) x[u] = y[u];
     }
-    if (tid < sl.n_edge)
+    if (tid < sl.n_edge && LQ_IN_RANGE(sl.c0 + sl.edge(tid), P.V))
       Log<T>::put(gs + sl.edge(tid), n.f_rest * ex2_from(z_edge, n.m_rest, P.c2));
     __syncthreads();
   }
