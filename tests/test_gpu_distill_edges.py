@@ -295,3 +295,30 @@ def test_not_a_number_reaches_the_loss(M, V, k, name):
             loss, grad = lq.lq_distill_loss(z, badt, ti, t_lse=t_lse, want_grad=True)
             assert loss[1].isnan() and not loss[0].isnan()
             assert grad[1].gather(0, ti[1, :n]).isnan().all()
+
+
+def test_a_replayed_graph_reads_its_inputs_anew():
+    """Logits, teacher values and indices, log-partition and weights copied in anew
+    between replays: nothing of the capture or of the replay before stays."""
+    M, V, k = 40, 5003, 32
+    batches = []
+    for seed in (1, 2, 3):
+        z, tv, ti, lse = apart(seed, M, V, k, torch.bfloat16, 2.0, 0.3)
+        batches.append((z, tv, ti, lse.float(), rand(seed + 9, M).abs()))
+    for tail in (False, True):
+        want = [lq.lq_distill_loss(z, tv, ti, t_lse=lse if tail else None, weight=w,
+                                   want_grad=True) for z, tv, ti, lse, w in batches]
+        held = [torch.zeros_like(t) for t in batches[0]]
+        loss, grad = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            lq.lq_distill_loss(held[0], held[1], held[2], t_lse=held[3] if tail else None,
+                               weight=held[4], loss=loss, grad=grad)
+        for i in (0, 1, 2, 0):
+            for t, src in zip(held, batches[i]):
+                t.copy_(src)
+            loss.fill_(float("nan")), grad.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(loss, want[i][0]) and torch.equal(grad, want[i][1])
+        assert not torch.equal(want[0][0], want[1][0])
