@@ -146,9 +146,9 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// logistic function through the hardware exponential and reciprocal (a few
-// units in the last place of float32, far below the 16-bit output rounding);
-// exp overflow gives 1/inf = 0
+// logistic function through the hardware exponential and reciprocal (off by about
+// 2^-22 + |z| 2^-23 of the value, its exponent being rounded: far below the 16-bit
+// output rounding); exp overflow gives 1/inf = 0
 __device__ __forceinline__ float logistic(float z) {
   return rcp(1.f + ex2(-1.4426950408889634f * z));
 }
@@ -161,8 +161,9 @@ __device__ __forceinline__ float gelu_tanh_gate(float z) {
 // tail is Q(a) = e P(1 / (1 + c a)), a = |z|, with a polynomial P without
 // constant term (Q(a) / e falls off as 1 / a) fitted to 0.5 erfcx(a / sqrt 2) by
 // weighted least squares over 0 <= a <= 14; Phi is Q or 1 - Q, so nothing cancels
-// at large negative z.  In float32 it is off by at most 1.3e-6 of the value and
-// 6e-7 absolute, against half a step of 4.9e-4 of an f16 output.
+// at large negative z.  In float32 it is off by at most 6e-7 absolute, and by 1.3e-6 of
+// the value above z = -3; below, the rounded exponent adds up to z^2 2^-23 of the value
+// (2.2e-6 down to -6, 7.7e-6 down to -13), against half a step of 4.9e-4 of an f16 output.
 __device__ __forceinline__ float phi_cdf(float z, float& e) {
   const float a = fabsf(z);
   const float t = rcp(fmaf(0.36f, a, 1.f));

@@ -550,15 +550,15 @@ __global__ void __launch_bounds__(kThreads, kCtas)
       // both sums in units of the larger maximum
       const float top = fmaxf(M, M2nd);
       to_top = M == top ? 0.0 : ((double)M - (double)top) * (double)P.c2;
-      const float up = to_top == 0.0 ? 1.f : exp2f((float)to_top);
-      total = S * (double)up + scaled(M2nd, second, top);
+      const double up = to_top == 0.0 ? 1.0 : exp2(to_top);
+      total = S * up + scaled(M2nd, second, top);
       // nothing outside the list: no rest class, neither in the loss nor in its gradient
       R = S != 0.0 && 1.0 - TS > 0.0 ? 1.0 - TS : 0.0;
       const double C = TS + R;
       const float scale = w * P.inv_temp, f = (float)C / (float)total;
       n.m = ref(top);
       n.m_rest = ref(M);
-      n.f_rest = S != 0.0 ? scale * (f * up - (float)R / (float)S) : 0.f;
+      n.f_rest = S != 0.0 ? scale * (f * (float)up - (float)R / (float)S) : 0.f;
       n.f_top = scale * f;
       n.inv_ts = n.tm = 0.f;
     } else {
