@@ -20,8 +20,8 @@
 // residual in float32, round once, and write whole 64-byte or longer row
 // pieces through a swizzled shared-memory tile.  Large products are bound by the
 // tensor pipe: a tile of CTA pairs takes the pipe's own 512 clocks per 64-wide
-// block, 16384 x 5632 x 2048 takes 250 us (1.51 PFLOP/s) and its gated form 472
-// (1.60); in a long series the power cap sets the clock.  One elected lane runs
+// block, 16384 x 5632 x 2048 takes 244 us (1.55 PFLOP/s) and its gated form 473
+// (1.60) in a short series; in a long one the power cap sets the clock.  One elected lane runs
 // the whole copy or MMA loop: an elected lane inside a loop of the whole warp took
 // 350 clocks per block of a 128 x 64 tile, a plain lane test 540, this form 285.
 // Where a long contraction has few tiles, a cluster of CTAs shares a tile: each takes
@@ -507,7 +507,7 @@ __device__ __forceinline__ void flush_unit(const unsigned char* stg, int lane, c
     // Rows that start anywhere: the aligned 16-byte vectors inside the row's piece,
     // each shifted together from two, and the eight elements before and after them
     // one by one (1003 x 49155 x 2048: 148 us; with 4-byte words 183, with elements
-    // 199).
+    // 199; short series, in a long one the first takes 192).
 #pragma unroll 4
     for (int j = 0; j < kPieces; ++j) {
       const int row = j * (32 / kPieces) + lane / kPieces, pc = lane % kPieces;

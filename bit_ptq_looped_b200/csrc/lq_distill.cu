@@ -26,9 +26,11 @@
 // gradient a second one that finds the row in L2, where the rows in flight (some
 // 100 KB each, four per SM) stay; the gradients are stored as streaming data so
 // as not to displace them.  Nothing limits the row's length, and nothing waits
-// but at barriers.  Measured, 8192 x 49152 bf16 logits: 209 us for the loss
-// (floor 123), 355 with the gradient (floor 246).  Holding the row in shared
-// memory between the passes (bulk copies in and out, two rows per SM) took 250
+// but at barriers.  Measured, 8192 x 49152 bf16 logits: 212 us for the loss
+// (floor 123), 355 with the gradient (floor 246) in a short series, 384 in a long one;
+// with a rest class, whose listed entries are hidden vector by vector, 239 and 387 (a
+// float maximum over the unpacked vector instead of the packed one took 4 more).  Holding
+// the row in shared memory between the passes (bulk copies in and out, two rows per SM) took 250
 // and 342-365, and 46-56 against 26 for the loss of 255 x 100003 float32 logits;
 // a ring of bulk copies running ahead across passes and rows took 600, and keeping
 // part of the row in shared memory 555: what shared memory takes, the L1 lines

@@ -440,7 +440,8 @@ lq_status lq_gated_linear_bwd(const void* d_dh, const void* d_g, const void* d_u
  *   d_t_values  M x k, t_dtype any of the three types; -inf counts nothing.
  *   d_t_index   M x k vocabulary indices, int32 (idx_bytes 4) or int64 (8).  An
  *               index outside [0, V) is no entry (padding of a shorter list);
- *               one that a row lists again counts at its first position.
+ *               one that a row lists again counts at its first position, and
+ *               costs that row up to k^2 / 2 comparisons.
  *   d_weight    M row weights (upstream gradient, 1 / rows, 0 for padding), or
  *               NULL for 1.  A row of weight 0, and without d_t_lse a row
  *               without an entry, has loss 0 and gradient 0 whatever its
